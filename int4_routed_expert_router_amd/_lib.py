@@ -16,6 +16,7 @@ MOE_GEMV_MAX_ROWS = 32
 MOE_POOL_HOST_ONLY = 1
 MOE_POOL_DMA_COPY = 2
 MOE_TIME_GATEUP, MOE_TIME_DOWN, MOE_TIME_ROUTER = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 1, 2
 MOE_FLAG_F16_RANGE = 1
 MOE_FLAG_STREAM_WAIT = 2
 
@@ -37,6 +38,11 @@ class LayerWeights(C.Structure):
 class GdnDesc(C.Structure):
     _fields_ = [("batch", C.c_int32), ("k_heads", C.c_int32), ("v_heads", C.c_int32), ("head_k_dim", C.c_int32),
                 ("head_v_dim", C.c_int32), ("act_dtype", C.c_int32)]
+
+
+class SelectDescC(C.Structure):
+    _fields_ = [("n_experts", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32), ("n_group", C.c_int32),
+                ("top_groups", C.c_int32), ("group_top", C.c_int32), ("renorm", C.c_int32), ("scale", C.c_float)]
 
 
 class SlotPoolConfig(C.Structure):
@@ -83,6 +89,8 @@ PROTOS = {
     "moe_graph_destroy": (None, [vp]),
     "moe_synth_fill_experts": (i32, [u64, i32, i32, i32, i32, i32, i32, i32, f32, f32, vp, u64, vp]),
     "moe_synth_philox": (i32, [vp, vp, vp, i32, vp]),
+    "moe_select": (i32, [C.POINTER(SelectDescC), vp, C.c_int64, vp, i32, vp, vp, vp, vp]),
+    "moe_route_scored": (i32, [vp, C.POINTER(SelectDescC), vp, vp, i32, vp, vp, vp, vp, vp, C.c_size_t, vp]),
     "moe_gdn_step": (i32, [C.POINTER(GdnDesc), vp, vp, vp, vp, vp, f32, vp, vp, vp]),
     "slotpool_create": (i32, [C.POINTER(SlotPoolConfig), C.POINTER(vp)]),
     "slotpool_acquire": (i32, [vp, i32, vp, i32, u64, vp, vp, vp, vp]),

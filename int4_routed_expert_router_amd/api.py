@@ -14,12 +14,14 @@ import numpy as np
 import torch
 
 from ._lib import (GdnDesc, MOE_BF16, MOE_F16, MOE_PATH_AUTO, MOE_POOL_DMA_COPY, MOE_POOL_HOST_ONLY, LayerDesc,  # noqa: F401
-                   LayerWeights, SlotPoolConfig, SlotPoolStats, check, lib)
+                   LayerWeights, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, SelectDescC, SlotPoolConfig, SlotPoolStats,
+                   check, lib)
 
 __all__ = ["Desc", "Layer", "blob_bytes", "pack_expert", "workspace_bytes", "workspace", "workspace_status",
            "route", "permute",
            "expert_ffn", "layer_forward", "layer_forward_static", "stack_epilogue", "stack_forward", "StackGraph", "synth_fill_experts",
-           "synth_philox", "SlotPool", "pool_decode_step", "DevPool", "pool_decode_step_dev", "PoolGraph", "gdn_step"]
+           "synth_philox", "SlotPool", "pool_decode_step", "DevPool", "pool_decode_step_dev", "PoolGraph", "gdn_step",
+           "SelectDesc", "select", "route_scored"]
 
 
 _ACT_DTYPES = (torch.int16, torch.float16, torch.bfloat16)
@@ -68,6 +70,33 @@ def _scratch(desc, T, device, stream):
     if stream is not None and stream != torch.cuda.current_stream(ws.device):
         ws.record_stream(stream)
     return ws
+
+
+def _device(ref, **others):
+    """Index of the device that ref and every other tensor given live on."""
+    dev = ref.device
+    for name, t in others.items():
+        if isinstance(t, torch.Tensor) and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    return dev.index
+
+
+def _stream_on(dev, stream):
+    """Handle of the stream (None: the current stream of device dev)."""
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    return _stream(stream)
+
+
+def _call_on(dev, fn, *args):
+    """Status check of a library call made with device dev current."""
+    if torch.cuda.current_device() == dev:
+        check(fn(*args))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args))
 
 
 def _tokens(x, desc, name="x"):
@@ -176,6 +205,61 @@ def route(desc, layer, x, topk_idx, topk_w, shared_gate=None, logits=None, ws=No
     d, w = desc.c(), layer.c()
     ws = _scratch(desc, T, x.device, stream) if ws is None else ws
     check(lib().moe_route(C.byref(d), C.byref(w), *args, _ws(ws), ws.numel(), _stream(stream)))
+
+
+@dataclasses.dataclass(frozen=True)
+class SelectDesc:
+    """How K of E experts are chosen from router logits (moe_select_desc)."""
+    n_experts: int
+    top_k: int
+    score: str = "softmax"           # "softmax" | "sigmoid"
+    n_group: int = 1
+    top_groups: int = 0              # 0: every group takes part
+    group_top: int = 1               # 1 | 2 best keys make a group's rank
+    renorm: bool = True
+    scale: float = 1.0
+
+    def c(self) -> SelectDescC:
+        d = self.__dict__.get("_c")
+        if d is None:
+            d = SelectDescC(self.n_experts, self.top_k,
+                            {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}.get(self.score, 0),
+                            self.n_group, self.top_groups, self.group_top, int(self.renorm), self.scale)
+            object.__setattr__(self, "_c", d)
+        return d
+
+
+def select(desc, logits, topk_idx, topk_w, bias=None, shared_gate=None, stream=None):
+    """Choice of K experts per token from given logits (moe_select): logits
+    [T, E], or [T, E+1] as route() writes them, fp32; bias [E] fp32 enters the
+    choice only; topk_idx [T, K] int32, topk_w [T, K] fp32; shared_gate [T]
+    fp32 = sigmoid of column E."""
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2:
+        raise ValueError("logits must be a [T, E] or [T, E+1] tensor")
+    E, K = desc.n_experts, desc.top_k
+    T, cols = logits.shape
+    if cols != E and cols != E + 1:
+        raise ValueError(f"logits has {cols} columns, expected {E} or {E + 1}")
+    args = (_ptr(logits, "logits", _F32), cols, _ptr(bias, "bias", _F32, E), T,
+            _ptr(topk_idx, "topk_idx", _I32, T * K), _ptr(topk_w, "topk_w", _F32, T * K),
+            _ptr(shared_gate, "shared_gate", _F32, T))
+    dev = _device(logits, bias=bias, topk_idx=topk_idx, topk_w=topk_w, shared_gate=shared_gate)
+    _call_on(dev, lib().moe_select, desc.c(), *args, _stream_on(dev, stream))
+
+
+def route_scored(desc, sel, layer, x, topk_idx, topk_w, shared_gate=None, logits=None, ws=None, stream=None):
+    """route() with the choice of a SelectDesc (moe_route_scored); the layer's
+    router_bias is the balance bias.  expert_ffn() takes the outputs."""
+    T = _tokens(x, desc)
+    K, E = desc.top_k, desc.n_experts
+    args = (_ptr(x), T, _ptr(topk_idx, "topk_idx", _I32, T * K), _ptr(topk_w, "topk_w", _F32, T * K),
+            _ptr(shared_gate, "shared_gate", _F32, T), _ptr(logits, "logits", _F32, T * (E + 1)))
+    dev = _device(x, topk_idx=topk_idx, topk_w=topk_w, shared_gate=shared_gate, logits=logits, ws=ws,
+                  router_w=layer.router_w, router_bias=layer.router_bias)
+    d, w = desc.c(), layer.c()
+    ws = _scratch(desc, T, x.device, stream) if ws is None else ws
+    _call_on(dev, lib().moe_route_scored, C.byref(d), sel.c(), C.byref(w), *args, _ws(ws), ws.numel(),
+             _stream_on(dev, stream))
 
 
 def permute(desc, topk_idx, expert_off, perm, inv=None, ws=None, stream=None):

@@ -10,7 +10,12 @@
 #include "moe_common.h"
 #include "moe.h"
 #include "moe_kernels.h"
+#include "moe_select.h"
 #include "moe_slotpool.h"
+
+namespace moe {
+moe_status check_select(const moe_select_desc* d, SelectArgs* a);   // moe_select.hip
+}
 
 namespace {
 
@@ -454,6 +459,44 @@ moe_status moe_route(const moe_layer_desc* d, const moe_layer_weights* w, const 
   st = do_route(d, w, x, T, topk_idx, topk_w, gamma, at<float>(ws, L.logits), logits_or_null,
                 reinterpret_cast<hipStream_t>(stream));
   return st ? st : ok();
+}
+
+moe_status moe_route_scored(const moe_layer_desc* d, const moe_select_desc* sel, const moe_layer_weights* w,
+                            const void* x, int32_t T, int32_t* topk_idx, float* topk_w, float* shared_gate,
+                            float* logits_or_null, void* ws, size_t ws_bytes, moe_stream stream) {
+  moe_status st = check_desc(d);
+  if (st) return st;
+  moe::SelectArgs a;
+  if ((st = moe::check_select(sel, &a))) return st;
+  if (sel->n_experts != d->n_experts || sel->top_k != d->top_k)
+    return fail(MOE_ESHAPE, "the select desc (%d of %d experts) differs from the layer's (%d of %d)", sel->top_k,
+                sel->n_experts, d->top_k, d->n_experts);
+  if ((st = check_weights(d, w))) return st;
+  if (T < 0) return fail(MOE_ESHAPE, "n_tokens=%d < 0", T);
+  if (T == 0) return ok();
+  if (!x || !aligned(x, 16)) return fail(MOE_EINVAL, "x must be a 16-byte aligned device pointer");
+  if (!topk_idx || !topk_w) return fail(MOE_EINVAL, "topk_idx and topk_w are required");
+  Ws L;
+  if ((st = check_ws(d, T, ws, ws_bytes, L))) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  // the balance bias must not enter the logits: the router runs without it
+  moe_layer_weights unbiased = *w;
+  unbiased.router_bias = nullptr;
+  moe::RouterParts rp{};
+  if ((st = do_router(d, &unbiased, x, T, at<float>(ws, L.logits), s, -1, &rp))) return st;
+  a.part = at<float>(ws, L.logits);
+  a.n_part = rp.n_part;
+  a.ld = d->n_experts + 1;
+  a.pstride = static_cast<int64_t>(T) * (d->n_experts + 1);
+  a.bias = w->router_bias;
+  a.T = T;
+  a.idx = topk_idx;
+  a.w = topk_w;
+  a.gamma = shared_gate;
+  a.logits = logits_or_null;
+  const hipError_t e = moe::launch_select(a, s);
+  if (e != hipSuccess) return hip_fail(e, "select kernel launch");
+  return ok();
 }
 
 moe_status moe_permute(const moe_layer_desc* d, const int32_t* topk_idx, int32_t T, int32_t* expert_off,

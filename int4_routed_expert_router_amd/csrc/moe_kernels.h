@@ -120,6 +120,21 @@ hipError_t launch_router_combine(int act, const uint16_t* wr, const float* bias,
 // non-null) and, when logits is non-null, the logits themselves.
 hipError_t launch_topk(const float* part, int n_part, const float* bias, int T, int E, int K, int32_t* idx, float* w,
                        float* gamma, float* logits, hipStream_t s);
+// Scored expert choice (see include/moe_select.h).  Logit (t, e) is the sum over
+// slices p < n_part of part[p * pstride + t * ld + e]; column E is the
+// shared-gate logit (read only when gamma or logits is non-null).
+struct SelectArgs {
+  const float* part;
+  int64_t ld, pstride;
+  const float* bias;      // [E] or nullptr
+  int32_t* idx;           // [T][K]
+  float* w;               // [T][K]
+  float* gamma;           // [T] or nullptr
+  float* logits;          // [T][E+1] copy of the summed logits, or nullptr
+  int n_part, T, E, K, score, n_group, top_groups, group_top, renorm;
+  float scale;
+};
+hipError_t launch_select(const SelectArgs& a, hipStream_t s);
 hipError_t launch_permute(const int32_t* idx, int n, int E, int32_t* off, int32_t* perm, int32_t* inv,
                           const UnitPlan* plan, hipStream_t s);
 
