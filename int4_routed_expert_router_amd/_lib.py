@@ -10,7 +10,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoe_amd.so")
 
 MOE_OK, MOE_EINVAL, MOE_ESHAPE, MOE_EWORKSPACE, MOE_EHIP, MOE_EPOOLFULL, MOE_EBUSY, MOE_ENOMEM = 0, -1, -2, -3, -4, -5, -6, -7
-MOE_F16, MOE_BF16 = 1, 2
+MOE_F16, MOE_BF16, MOE_F32 = 1, 2, 3
 MOE_PATH_AUTO, MOE_PATH_GEMV, MOE_PATH_GROUPED = 0, 1, 2
 MOE_GEMV_MAX_ROWS = 32
 MOE_POOL_HOST_ONLY = 1
@@ -43,6 +43,11 @@ class GdnDesc(C.Structure):
 class SelectDescC(C.Structure):
     _fields_ = [("n_experts", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32), ("n_group", C.c_int32),
                 ("top_groups", C.c_int32), ("group_top", C.c_int32), ("renorm", C.c_int32), ("scale", C.c_float)]
+
+
+class LinearDesc(C.Structure):
+    _fields_ = [("in_dim", C.c_int32), ("out_dim", C.c_int32), ("group_size", C.c_int32), ("act_dtype", C.c_int32),
+                ("out_dtype", C.c_int32)]
 
 
 class SlotPoolConfig(C.Structure):
@@ -91,6 +96,9 @@ PROTOS = {
     "moe_synth_philox": (i32, [vp, vp, vp, i32, vp]),
     "moe_select": (i32, [C.POINTER(SelectDescC), vp, C.c_int64, vp, i32, vp, vp, vp, vp]),
     "moe_route_scored": (i32, [vp, C.POINTER(SelectDescC), vp, vp, i32, vp, vp, vp, vp, vp, C.c_size_t, vp]),
+    "moe_linear_bytes": (u64, [i32, i32, i32]),
+    "moe_linear_pack": (i32, [i32, i32, i32, vp, vp, vp, vp, vp]),
+    "moe_linear_forward": (i32, [C.POINTER(LinearDesc), vp, vp, i32, vp, vp]),
     "moe_gdn_step": (i32, [C.POINTER(GdnDesc), vp, vp, vp, vp, vp, f32, vp, vp, vp]),
     "slotpool_create": (i32, [C.POINTER(SlotPoolConfig), C.POINTER(vp)]),
     "slotpool_acquire": (i32, [vp, i32, vp, i32, u64, vp, vp, vp, vp]),

@@ -13,7 +13,7 @@ import dataclasses
 import numpy as np
 import torch
 
-from ._lib import (GdnDesc, MOE_BF16, MOE_F16, MOE_PATH_AUTO, MOE_POOL_DMA_COPY, MOE_POOL_HOST_ONLY, LayerDesc,  # noqa: F401
+from ._lib import (GdnDesc, LinearDesc, MOE_BF16, MOE_F16, MOE_F32, MOE_PATH_AUTO, MOE_POOL_DMA_COPY, MOE_POOL_HOST_ONLY, LayerDesc,  # noqa: F401
                    LayerWeights, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, SelectDescC, SlotPoolConfig, SlotPoolStats,
                    check, lib)
 
@@ -21,7 +21,7 @@ __all__ = ["Desc", "Layer", "blob_bytes", "pack_expert", "workspace_bytes", "wor
            "route", "permute",
            "expert_ffn", "layer_forward", "layer_forward_static", "stack_epilogue", "stack_forward", "StackGraph", "synth_fill_experts",
            "synth_philox", "SlotPool", "pool_decode_step", "DevPool", "pool_decode_step_dev", "PoolGraph", "gdn_step",
-           "SelectDesc", "select", "route_scored"]
+           "SelectDesc", "select", "route_scored", "Linear", "linear"]
 
 
 _ACT_DTYPES = (torch.int16, torch.float16, torch.bfloat16)
@@ -489,6 +489,56 @@ def gdn_step(q, k, v, g, beta, state, o, q_scale, act_dtype="bf16", stream=None)
     d = GdnDesc(B, Hk, Hv, dk, dv, {"bf16": MOE_BF16, "f16": MOE_F16}.get(act_dtype, 0))
     check(lib().moe_gdn_step(C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(q_scale), _ptr(state),
                              _ptr(o), _stream(stream)))
+
+
+_OUT = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+
+
+class Linear:
+    """int4 affine group-quantised weights of a dense product, laid out on
+    the device once (moe_linear_pack).
+
+    words: [out, in/8] int32, value 8i + j of a row in bits 4j..4j+3 of its
+    word i; scale, bias: [out, in/group] float16 (or int16 bits); act_dtype:
+    dtype of the activations, "f16" | "bf16".  The source tensors may be
+    freed once the pack call's stream has passed it."""
+
+    def __init__(self, in_dim, out_dim, group_size, words, scale, bias, act_dtype="bf16", stream=None):
+        n = int(lib().moe_linear_bytes(in_dim, out_dim, group_size))
+        if n == 0:
+            raise ValueError(f"unsupported linear in={in_dim} out={out_dim} group={group_size}")
+        if act_dtype not in ("f16", "bf16"):
+            raise ValueError(f"act_dtype {act_dtype!r} is not 'f16' or 'bf16'")
+        f16 = (torch.float16, torch.int16)
+        ng = out_dim * (in_dim // group_size)
+        args = (_ptr(words, "words", _I32, out_dim * in_dim // 8), _ptr(scale, "scale", f16, ng),
+                _ptr(bias, "bias", f16, ng))
+        if any(a is None for a in args):
+            raise ValueError("words, scale and bias are required")
+        dev = _device(words, scale=scale, bias=bias)
+        self.in_dim, self.out_dim, self.group_size, self.act_dtype = in_dim, out_dim, group_size, act_dtype
+        self.packed = torch.empty(n, dtype=torch.uint8, device=words.device)
+        act = {"bf16": MOE_BF16, "f16": MOE_F16}[act_dtype]
+        self._c = {t: LinearDesc(in_dim, out_dim, group_size, act, o) for t, o in _OUT.items()}
+        _call_on(dev, lib().moe_linear_pack, in_dim, out_dim, group_size, *args, self.packed.data_ptr(),
+                 _stream_on(dev, stream))
+        if isinstance(stream, torch.cuda.Stream):
+            self.packed.record_stream(stream)
+
+
+def linear(lin, x, y, stream=None):
+    """y = x W^T (moe_linear_forward): x [T, in] in the linear's act_dtype (or
+    int16 bits), y [T, out] float16, bfloat16 or float32."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be a [T, in] tensor")
+    if not isinstance(y, torch.Tensor) or y.dtype not in _OUT:
+        raise ValueError("y must be a float16, bfloat16 or float32 tensor")
+    T = x.shape[0]
+    act = torch.bfloat16 if lin.act_dtype == "bf16" else torch.float16
+    args = (lin.packed.data_ptr(), _ptr(x, "x", (act, torch.int16), T * lin.in_dim), T,
+            _ptr(y, "y", None, T * lin.out_dim))
+    dev = _device(x, y=y, weights=lin.packed)
+    _call_on(dev, lib().moe_linear_forward, lin._c[y.dtype], *args, _stream_on(dev, stream))
 
 
 def synth_fill_experts(seed, layer, expert_first, n_experts, hidden, inter, group, scale_lo, scale_hi, dst, stride,

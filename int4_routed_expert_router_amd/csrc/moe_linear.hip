@@ -1,0 +1,251 @@
+// Dense products with int4 affine group-quantised weights (see
+// include/moe_linear.h for the formula and the packed layout).
+//
+// On the matrix cores the weight operand is v = 1 + q/16, exact in fp16 and
+// bf16 (two logic operations per pair of nibbles), so per group of columns
+//   sum q x = 16 sum v x - 16 sum x,
+//   y += 16 s (sum v x) + (b - 16 s) (sum x),
+// with both sums in fp32; sum x comes from the same matrix instruction with
+// an operand of ones.  Tokens are the tile's rows and weight rows its
+// columns, so a lane needs the scale and bias of one weight row per tile.
+#include <hip/hip_runtime.h>
+
+#include "moe_common.h"
+#include "moe_linear.h"
+
+namespace moe {
+moe_status set_error(moe_status code, const char* fmt, ...);
+
+namespace {
+
+bool lin_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+template <int ACT>
+__device__ __forceinline__ f32x4 mfma32(uint4 a, uint4 b, f32x4 c) {
+  if constexpr (ACT == 2)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                  0);
+}
+template <int ACT>
+__device__ __forceinline__ uint4 v_operand(uint32_t w) {
+  return make_uint4(q_pair<ACT>(w, 0), q_pair<ACT>(w, 1), q_pair<ACT>(w, 2), q_pair<ACT>(w, 3));
+}
+template <int ACT>
+__device__ __forceinline__ uint4 ones_operand() {
+  constexpr uint32_t one = ACT == 2 ? 0x3F803F80u : 0x3C003C00u;
+  return make_uint4(one, one, one, one);
+}
+
+template <int RES>
+__device__ __forceinline__ void store_out(void* y, size_t i, float v) {
+  if constexpr (RES == 3) static_cast<float*>(y)[i] = v;
+  else static_cast<uint16_t*>(y)[i] = f32_to_act<RES>(v);
+}
+
+constexpr int kLinWaves = 8;    // waves of a workgroup, each on every 8th 64-column chunk
+constexpr int kLinBatch = 4;    // chunks whose loads a wave issues together
+
+// One workgroup: 32 weight rows (pair-tile blockIdx.x) x 16 TT tokens
+// (blockIdx.y).  The waves split the columns; their fp32 partial tiles are
+// added in wave order.
+template <int ACT, int RES, int TT, bool G32>
+__global__ __launch_bounds__(64 * kLinWaves) void k_linear(const uint8_t* __restrict__ packed,
+                                                           const uint16_t* __restrict__ x, void* __restrict__ y, int T,
+                                                           int N, int K, int G, uint64_t scale_off) {
+  __shared__ float red[kLinWaves][TT * 8][64];
+  const int lane = threadIdx.x & 63, n = lane & 15, kb = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int p = blockIdx.x, nc = K / 64, ng = K / G;
+  const uint4* wq = reinterpret_cast<const uint4*>(packed + static_cast<uint64_t>(p) * nc * 1024) + lane;
+  const uint8_t* sec = packed + scale_off;
+  const uint16_t* xr[TT];
+#pragma unroll
+  for (int tt = 0; tt < TT; ++tt)   // rows past the last token read the last one; their results are not stored
+    xr[tt] = x + static_cast<size_t>(min(static_cast<int>(blockIdx.y) * 16 * TT + 16 * tt + n, T - 1)) * K + 8 * kb;
+  f32x4 acc[TT][2];
+#pragma unroll
+  for (int tt = 0; tt < TT; ++tt) acc[tt][0] = acc[tt][1] = f32x4{0, 0, 0, 0};
+  const uint4 ones = ones_operand<ACT>();
+  for (int c0 = wave; c0 < nc; c0 += kLinWaves * kLinBatch) {
+    uint4 w[kLinBatch];
+    ScaleBias sb[kLinBatch][G32 ? 2 : 1];
+#pragma unroll
+    for (int u = 0; u < kLinBatch; ++u) {
+      const int c = min(c0 + u * kLinWaves, nc - 1);
+      w[u] = wq[static_cast<size_t>(c) * 64];
+      if constexpr (G32) {
+        sb[u][0] = load_sb(sec, p, ng, 2 * c, n);
+        sb[u][1] = load_sb(sec, p, ng, 2 * c + 1, n);
+      } else {
+        sb[u][0] = load_sb(sec, p, ng, G == 128 ? c >> 1 : c, n);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kLinBatch; ++u) {
+      const int c = c0 + u * kLinWaves;
+      if (c >= nc) break;   // wave-uniform
+      const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      f32x4 ga[TT], gb[TT], gx[TT];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const uint4 va = v_operand<ACT>(ww[ks]), vb = v_operand<ACT>(ww[2 + ks]);
+        const bool fresh = G32 || ks == 0;
+#pragma unroll
+        for (int tt = 0; tt < TT; ++tt) {
+          const uint4 xv = *reinterpret_cast<const uint4*>(xr[tt] + 64 * c + 32 * ks);
+          const f32x4 zero = {0, 0, 0, 0};
+          ga[tt] = mfma32<ACT>(xv, va, fresh ? zero : ga[tt]);
+          gb[tt] = mfma32<ACT>(xv, vb, fresh ? zero : gb[tt]);
+          gx[tt] = mfma32<ACT>(xv, ones, fresh ? zero : gx[tt]);
+        }
+        if (G32 || ks == 1) {
+          const ScaleBias s = sb[u][G32 ? ks : 0];
+          const float sa = 16.0f * s.sA, sB = 16.0f * s.sB, ba = s.bA - sa, bB = s.bB - sB;
+#pragma unroll
+          for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              acc[tt][0][i] = fmaf(sa, ga[tt][i], fmaf(ba, gx[tt][i], acc[tt][0][i]));
+              acc[tt][1][i] = fmaf(sB, gb[tt][i], fmaf(bB, gx[tt][i], acc[tt][1][i]));
+            }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int tt = 0; tt < TT; ++tt)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[wave][tt * 8 + i][lane] = acc[tt][i >> 2][i & 3];
+  __syncthreads();
+  for (int r = wave; r < TT * 8; r += kLinWaves) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kLinWaves; ++w) v += red[w][r][lane];
+    const int t = static_cast<int>(blockIdx.y) * 16 * TT + 16 * (r >> 3) + 4 * kb + (r & 3);
+    const int col = 32 * p + 16 * ((r >> 2) & 1) + n;
+    if (t < T && col < N) store_out<RES>(y, static_cast<size_t>(t) * N + col, v);
+  }
+}
+
+// One thread per packed word (values), then one per 8-byte scale entry.
+__global__ __launch_bounds__(256) void k_linear_pack(const uint32_t* __restrict__ q, const uint16_t* __restrict__ s,
+                                                     const uint16_t* __restrict__ b, uint8_t* __restrict__ packed,
+                                                     int N, int K, int G, uint64_t n_words, uint64_t n_scales) {
+  const uint64_t i = static_cast<uint64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i < n_words) {
+    const int wd = i & 3, lane = (i >> 2) & 63;
+    const uint64_t blk = i >> 8;
+    const int nc = K / 64, c = static_cast<int>(blk % nc);
+    const int64_t row = static_cast<int64_t>(blk / nc) * 32 + 16 * (wd >> 1) + (lane & 15);
+    uint32_t out = 0;
+    if (row < N) {
+      const uint32_t in = q[row * (K / 8) + 8 * c + 4 * (wd & 1) + (lane >> 4)];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out |= ((in >> (4 * j)) & 15u) << (4 * ((j >> 1) + 4 * (j & 1)));
+    }
+    reinterpret_cast<uint32_t*>(packed)[i] = out;
+  } else if (i - n_words < n_scales) {
+    const uint64_t k = i - n_words;
+    const int n = k & 15, ng = K / G;
+    const uint64_t pg = k >> 4;
+    const int g = static_cast<int>(pg % ng);
+    const int64_t ra = static_cast<int64_t>(pg / ng) * 32 + n, rb = ra + 16;
+    uint32_t lo = 0, hi = 0;
+    if (ra < N) lo = s[ra * ng + g] | (static_cast<uint32_t>(b[ra * ng + g]) << 16);
+    if (rb < N) hi = s[rb * ng + g] | (static_cast<uint32_t>(b[rb * ng + g]) << 16);
+    reinterpret_cast<uint2*>(packed + 4 * n_words)[k] = make_uint2(lo, hi);
+  }
+}
+
+constexpr int kLinMaxIn = 65536, kLinMaxOut = 1 << 20, kLinMaxTokens = 1 << 20;
+
+bool linear_shape_ok(int K, int N, int G) {
+  return K >= 64 && K <= kLinMaxIn && K % 64 == 0 && N >= 1 && N <= kLinMaxOut &&
+         (G == 32 || G == 64 || G == 128) && K % G == 0;
+}
+uint64_t padded_rows(int N) { return (static_cast<uint64_t>(N) + 31) / 32 * 32; }
+
+template <int ACT, int RES>
+hipError_t launch_linear(const moe_linear_desc* d, const uint8_t* packed, const uint16_t* x, int T, void* y,
+                         hipStream_t s) {
+  const int K = d->in_dim, N = d->out_dim, G = d->group_size;
+  const uint64_t off = padded_rows(N) * K / 2;
+  const int tt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  const dim3 grid((N + 31) / 32, (T + 16 * tt - 1) / (16 * tt)), block(64 * kLinWaves);
+#define LIN(TT)                                                                                             \
+  do {                                                                                                      \
+    if (G == 32) hipLaunchKernelGGL((k_linear<ACT, RES, TT, true>), grid, block, 0, s, packed, x, y, T, N, K, G, off); \
+    else hipLaunchKernelGGL((k_linear<ACT, RES, TT, false>), grid, block, 0, s, packed, x, y, T, N, K, G, off);        \
+  } while (0)
+  if (tt == 1) LIN(1);
+  else if (tt == 2) LIN(2);
+  else LIN(4);
+#undef LIN
+  return hipGetLastError();
+}
+template <int ACT>
+hipError_t launch_linear_res(const moe_linear_desc* d, const uint8_t* packed, const uint16_t* x, int T, void* y,
+                             hipStream_t s) {
+  switch (d->out_dtype) {
+    case MOE_F16: return launch_linear<ACT, MOE_F16>(d, packed, x, T, y, s);
+    case MOE_BF16: return launch_linear<ACT, MOE_BF16>(d, packed, x, T, y, s);
+    default: return launch_linear<ACT, MOE_F32>(d, packed, x, T, y, s);
+  }
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" uint64_t moe_linear_bytes(int32_t K, int32_t N, int32_t G) {
+  if (!moe::linear_shape_ok(K, N, G)) return 0;
+  const uint64_t rows = moe::padded_rows(N);
+  return rows * K / 2 + 4 * rows * (K / G);
+}
+
+extern "C" moe_status moe_linear_pack(int32_t K, int32_t N, int32_t G, const uint32_t* q, const uint16_t* scale,
+                                      const uint16_t* bias, uint8_t* packed, moe_stream stream) {
+  using moe::set_error;
+  if (!moe::linear_shape_ok(K, N, G)) return set_error(MOE_ESHAPE, "unsupported linear in=%d out=%d group=%d", K, N, G);
+  if (!q || !scale || !bias) return set_error(MOE_EINVAL, "q, scale and bias are required");
+  if (!moe::lin_aligned(q, 4) || !packed || !moe::lin_aligned(packed, 256))
+    return set_error(MOE_EINVAL, "q must be 4-byte and packed a 256-byte aligned device pointer");
+  const uint64_t rows = moe::padded_rows(N), nw = rows * K / 8, ns = rows / 2 * (K / G);
+  const uint64_t blocks = (nw + ns + 255) / 256;
+  hipLaunchKernelGGL(moe::k_linear_pack, dim3(static_cast<uint32_t>(blocks)), dim3(256), 0,
+                     reinterpret_cast<hipStream_t>(stream), q, scale, bias, packed, N, K, G, nw, ns);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return set_error(MOE_EHIP, "linear pack kernel launch: %s", hipGetErrorString(e));
+  return set_error(MOE_OK, "");
+}
+
+extern "C" moe_status moe_linear_forward(const moe_linear_desc* d, const uint8_t* packed, const void* x, int32_t T,
+                                         void* y, moe_stream stream) {
+  using moe::set_error;
+  if (!d) return set_error(MOE_EINVAL, "desc is NULL");
+  if (!moe::linear_shape_ok(d->in_dim, d->out_dim, d->group_size))
+    return set_error(MOE_ESHAPE, "unsupported linear in=%d out=%d group=%d", d->in_dim, d->out_dim, d->group_size);
+  if (d->act_dtype != MOE_F16 && d->act_dtype != MOE_BF16)
+    return set_error(MOE_EINVAL, "act_dtype=%d is not MOE_F16/MOE_BF16", d->act_dtype);
+  if (d->out_dtype != MOE_F16 && d->out_dtype != MOE_BF16 && d->out_dtype != MOE_F32)
+    return set_error(MOE_EINVAL, "out_dtype=%d is not MOE_F16/MOE_BF16/MOE_F32", d->out_dtype);
+  if (T < 0 || T > moe::kLinMaxTokens) return set_error(MOE_ESHAPE, "n_tokens=%d must be in [0, %d]", T, moe::kLinMaxTokens);
+  if (T == 0) return set_error(MOE_OK, "");
+  if (!packed || !moe::lin_aligned(packed, 256))
+    return set_error(MOE_EINVAL, "packed must be a 256-byte aligned device pointer");
+  if (!x || !moe::lin_aligned(x, 16)) return set_error(MOE_EINVAL, "x must be a 16-byte aligned device pointer");
+  if (!y || !moe::lin_aligned(y, d->out_dtype == MOE_F32 ? 4 : 2))
+    return set_error(MOE_EINVAL, "y must be a device pointer aligned to its type");
+  const auto* xb = static_cast<const uint16_t*>(x);
+  const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  const hipError_t e = d->act_dtype == MOE_BF16 ? moe::launch_linear_res<MOE_BF16>(d, packed, xb, T, y, s)
+                                                : moe::launch_linear_res<MOE_F16>(d, packed, xb, T, y, s);
+  if (e != hipSuccess) return set_error(MOE_EHIP, "linear kernel launch: %s", hipGetErrorString(e));
+  return set_error(MOE_OK, "");
+}
