@@ -1,6 +1,6 @@
 /*
- * moe_gdn.h - Gated DeltaNet single-token recurrence (the step that runs
- * beside the MoE block).
+ * moe_gdn.h - Gated DeltaNet recurrence (the linear attention that runs
+ * beside the MoE block): one token per sequence, or whole sequences.
  *
  * Three quarters of the layers of the models this library serves use Gated
  * DeltaNet linear attention with a fixed-size recurrent state instead of a
@@ -51,6 +51,30 @@ typedef struct {
  * act_dtype; nothing is enqueued then. */
 moe_status moe_gdn_step(const moe_gdn_desc* desc, const void* q, const void* k, const void* v, const float* g,
                         const float* beta, float q_scale, float* state, float* o, moe_stream stream);
+
+/* The same rule over whole sequences (prompts, or several drafted tokens):
+ * the tokens of B sequences lie one after the other in q, k, v, g, beta and o
+ * ([n_tokens][heads]... as above, token rows instead of sequence rows), and
+ * sequence b owns tokens seq_off[b] .. seq_off[b+1] - 1 (device int32 [B+1],
+ * non-decreasing, within [0, n_tokens]).  state [B][v_heads][d_v][d_k] holds
+ * each sequence's state on entry and after its last token on exit; a sequence
+ * without tokens keeps its state.  Rows of o outside every sequence are left
+ * as they are.  Offsets outside the range are read as its nearest end, and an
+ * end before its start as an empty sequence; results of overlapping sequences
+ * are not defined.
+ *
+ * desc->batch is B; q, k 16-byte aligned; n_tokens up to 2^30.  The workspace
+ * (256-byte aligned, moe_gdn_prefill_workspace_bytes) is only used while the
+ * call runs.  State and sums are fp32; the results are those of the tokens
+ * taken one by one up to fp32 rounding, bitwise repeatable, and a sequence's
+ * results do not depend on the other sequences.  g <= 0 is expected (any g
+ * whose sums stay in fp32's exponent range works; -inf clears the state); a
+ * non-finite k, v, beta or g makes that sequence's results unusable from the
+ * start of its 64-token block on. */
+moe_status moe_gdn_prefill_workspace_bytes(const moe_gdn_desc* desc, int32_t n_tokens, size_t* bytes);
+moe_status moe_gdn_prefill(const moe_gdn_desc* desc, const int32_t* seq_off, int32_t n_tokens, const void* q,
+                           const void* k, const void* v, const float* g, const float* beta, float q_scale,
+                           float* state, float* o, void* ws, size_t ws_bytes, moe_stream stream);
 
 #ifdef __cplusplus
 }

@@ -100,6 +100,8 @@ PROTOS = {
     "moe_linear_pack": (i32, [i32, i32, i32, vp, vp, vp, vp, vp]),
     "moe_linear_forward": (i32, [C.POINTER(LinearDesc), vp, vp, i32, vp, vp]),
     "moe_gdn_step": (i32, [C.POINTER(GdnDesc), vp, vp, vp, vp, vp, f32, vp, vp, vp]),
+    "moe_gdn_prefill_workspace_bytes": (i32, [C.POINTER(GdnDesc), i32, C.POINTER(C.c_size_t)]),
+    "moe_gdn_prefill": (i32, [C.POINTER(GdnDesc), vp, i32, vp, vp, vp, vp, vp, f32, vp, vp, vp, C.c_size_t, vp]),
     "slotpool_create": (i32, [C.POINTER(SlotPoolConfig), C.POINTER(vp)]),
     "slotpool_acquire": (i32, [vp, i32, vp, i32, u64, vp, vp, vp, vp]),
     "slotpool_prefetch": (i32, [vp, i32, vp, i32, u64, vp, vp, vp, vp, vp]),

@@ -21,9 +21,11 @@ __all__ = ["Desc", "Layer", "blob_bytes", "pack_expert", "workspace_bytes", "wor
            "route", "permute",
            "expert_ffn", "layer_forward", "layer_forward_static", "stack_epilogue", "stack_forward", "StackGraph", "synth_fill_experts",
            "synth_philox", "SlotPool", "pool_decode_step", "DevPool", "pool_decode_step_dev", "PoolGraph", "gdn_step",
-           "SelectDesc", "select", "route_scored", "Linear", "linear"]
+           "SelectDesc", "select", "route_scored", "Linear", "linear", "gdn_prefill",
+           "gdn_prefill_workspace"]
 
 
+_ACT = {"bf16": MOE_BF16, "f16": MOE_F16}
 _ACT_DTYPES = (torch.int16, torch.float16, torch.bfloat16)
 
 
@@ -489,6 +491,41 @@ def gdn_step(q, k, v, g, beta, state, o, q_scale, act_dtype="bf16", stream=None)
     d = GdnDesc(B, Hk, Hv, dk, dv, {"bf16": MOE_BF16, "f16": MOE_F16}.get(act_dtype, 0))
     check(lib().moe_gdn_step(C.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(q_scale), _ptr(state),
                              _ptr(o), _stream(stream)))
+
+
+def gdn_prefill_workspace(n_seqs, n_tokens, k_heads, v_heads, head_v_dim, act_dtype="bf16", head_k_dim=128,
+                          device="cuda"):
+    """Workspace of gdn_prefill for up to n_seqs sequences of n_tokens tokens in all."""
+    d = GdnDesc(n_seqs, k_heads, v_heads, head_k_dim, head_v_dim, _ACT.get(act_dtype, 0))
+    n = C.c_size_t(0)
+    check(lib().moe_gdn_prefill_workspace_bytes(C.byref(d), n_tokens, C.byref(n)))
+    return torch.empty(max(int(n.value), 256), dtype=torch.uint8, device=device)
+
+
+def gdn_prefill(q, k, v, g, beta, state, o, seq_off, q_scale, act_dtype="bf16", ws=None, stream=None):
+    """Gated DeltaNet over whole sequences (moe_gdn_prefill): the tokens of B
+    sequences one after the other in q, k [N, Hk, 128], v [N, Hv, dv] (16-bit
+    tensors), g, beta [N, Hv] fp32 and o [N, Hv, dv] fp32; seq_off [B+1] int32
+    on the device; state [B, Hv, dv, 128] fp32, updated in place."""
+    for name, t, dims in (("q", q, 3), ("v", v, 3), ("state", state, 4)):
+        if not isinstance(t, torch.Tensor) or t.dim() != dims:
+            raise ValueError(f"{name} must be a tensor of {dims} dimensions")
+    N, Hk, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[2]
+    B = state.shape[0]
+    acts = {"bf16": (torch.bfloat16, torch.int16), "f16": (torch.float16, torch.int16)}.get(act_dtype, _ACT_DTYPES)
+    args = (_ptr(seq_off, "seq_off", _I32, B + 1), N, _ptr(q, "q", acts), _ptr(k, "k", acts, N * Hk * dk),
+            _ptr(v, "v", acts, N * Hv * dv), _ptr(g, "g", _F32, N * Hv), _ptr(beta, "beta", _F32, N * Hv),
+            float(q_scale), _ptr(state, "state", _F32, B * Hv * dv * dk), _ptr(o, "o", _F32, N * Hv * dv))
+    dev = _device(q, k=k, v=v, g=g, beta=beta, state=state, o=o, seq_off=seq_off, ws=ws)
+    d = GdnDesc(B, Hk, Hv, dk, dv, _ACT.get(act_dtype, 0))
+    if ws is None:
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            raise ValueError("pass ws explicitly when stream is a raw stream handle")
+        ws = gdn_prefill_workspace(B, N, Hk, Hv, dv, act_dtype, dk, q.device)
+        if stream is not None and stream != torch.cuda.current_stream(ws.device):
+            ws.record_stream(stream)
+    _call_on(dev, lib().moe_gdn_prefill, C.byref(d), *args, _ws(ws), ws.numel(), _stream_on(dev, stream))
 
 
 _OUT = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}

@@ -55,3 +55,18 @@ def gdn_step(state, q, k, v, g, beta, q_scale: float):
     new = alpha[..., None] * S + delta[..., :, None] * kn[..., None, :]
     o = np.einsum("bhij,bhj->bhi", new, qn)
     return new, o
+
+
+def gdn_sequences(state, q, k, v, g, beta, q_scale: float, lens):
+    """The step's rule over packed sequences of the given lengths: state
+    [B, Hv, dv, dk]; q, k [N, Hk, dk]; v [N, Hv, dv]; g, beta [N, Hv].
+    Returns (new_state, o [N, Hv, dv])."""
+    S = np.asarray(state, np.float64).copy()
+    o = np.zeros(np.shape(v), np.float64)
+    t = 0
+    for b, n in enumerate(lens):
+        for _ in range(n):
+            S[b:b + 1], o[t] = (lambda r: (r[0], r[1][0]))(
+                gdn_step(S[b:b + 1], q[t:t + 1], k[t:t + 1], v[t:t + 1], g[t:t + 1], beta[t:t + 1], q_scale))
+            t += 1
+    return S, o
