@@ -30,38 +30,43 @@ __device__ __forceinline__ void seq_range(const GdnArgs& a, int b, int& begin, i
   end = max(min(max(a.off[b + 1], 0), a.N), begin);
 }
 
-// Token by token: one workgroup per (16 state rows, value head, sequence); a
-// row of 16 lanes owns one state row in registers, lane l16 its columns
-// 8 l16 .. 8 l16 + 7.
-template <int ACT>
-__global__ __launch_bounds__(256) void k_gdn_tokens(GdnArgs a) {
-  const int slices = a.dv / 16;
-  const int h = blockIdx.x / slices, row = (blockIdx.x % slices) * 16 + (threadIdx.x >> 4);
-  const int b = blockIdx.y, hk = h / (a.Hv / a.Hk), c0 = 8 * (threadIdx.x & 15);
-  int t0, t1;
-  seq_range(a, b, t0, t1);
-  if (t0 == t1) return;
-  float* srow = a.state + ((static_cast<size_t>(b) * a.Hv + h) * a.dv + row) * kDK + c0;
-  float s[8];
-  *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(srow);
-  *reinterpret_cast<float4*>(s + 4) = *reinterpret_cast<const float4*>(srow + 4);
+// ---- token by token ---------------------------------------------------------
+// A row of 16 lanes owns NS state rows in registers (rows row0 + 16 z), lane
+// l16 their columns 8 l16 .. 8 l16 + 7.  Runs tokens [t0, t1) of one sequence
+// and value head.
+template <int ACT, int NS>
+__device__ __forceinline__ void run_tokens(const GdnArgs& a, int b, int h, int t0, int t1, int row0) {
+  const int hk = h / (a.Hv / a.Hk), c0 = 8 * (threadIdx.x & 15);
+  float* srow[NS];
+  float s[NS][8];
+#pragma unroll
+  for (int z = 0; z < NS; ++z) {
+    const int row = min(row0 + 16 * z, a.dv - 1);
+    srow[z] = a.state + ((static_cast<size_t>(b) * a.Hv + h) * a.dv + row) * kDK + c0;
+    *reinterpret_cast<float4*>(s[z]) = *reinterpret_cast<const float4*>(srow[z]);
+    *reinterpret_cast<float4*>(s[z] + 4) = *reinterpret_cast<const float4*>(srow[z] + 4);
+  }
   uint4 qv, kv;
-  uint32_t vv;
+  uint32_t vv[NS];
   float gv, bv;
   auto load = [&](int t) {
     const size_t qk = (static_cast<size_t>(t) * a.Hk + hk) * kDK + c0, hv = static_cast<size_t>(t) * a.Hv + h;
     qv = *reinterpret_cast<const uint4*>(a.q + qk);
     kv = *reinterpret_cast<const uint4*>(a.k + qk);
-    vv = a.v[hv * a.dv + row];
+#pragma unroll
+    for (int z = 0; z < NS; ++z) vv[z] = a.v[hv * a.dv + min(row0 + 16 * z, a.dv - 1)];
     gv = a.g[hv];
     bv = a.beta[hv];
   };
   load(t0);
   for (int t = t0; t < t1; ++t) {
     const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, kw[4] = {kv.x, kv.y, kv.z, kv.w};
-    const float alpha = expf(gv), bt = bv, vt = act_to_f32<ACT>(vv);
+    const float alpha = expf(gv), bt = bv;
+    float vt[NS];
+#pragma unroll
+    for (int z = 0; z < NS; ++z) vt[z] = act_to_f32<ACT>(vv[z]);
     load(min(t + 1, t1 - 1));
-    float qn[8], kn[8], qq = 0, kk = 0, kq = 0, u = 0, w = 0;
+    float qn[8], kn[8], qq = 0, kk = 0, kq = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       qn[j] = act_to_f32<ACT>((qw[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
@@ -69,22 +74,706 @@ __global__ __launch_bounds__(256) void k_gdn_tokens(GdnArgs a) {
       qq = fmaf(qn[j], qn[j], qq);
       kk = fmaf(kn[j], kn[j], kk);
       kq = fmaf(kn[j], qn[j], kq);
-      u = fmaf(s[j], kn[j], u);
-      w = fmaf(s[j], qn[j], w);
     }
     qq = row_sum16(qq);
     kk = row_sum16(kk);
     kq = row_sum16(kq);
-    u = row_sum16(u);
-    w = row_sum16(w);
     const float rq = a.q_scale / sqrtf(qq + kEps), rk = 1.0f / sqrtf(kk + kEps);
-    const float d = bt * (vt - alpha * (u * rk)), dk = d * rk;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = fmaf(dk, kn[j], alpha * s[j]);
-    if (c0 == 0) a.o[(static_cast<size_t>(t) * a.Hv + h) * a.dv + row] = fmaf(dk * rq, kq, alpha * (w * rq));
+    for (int z = 0; z < NS; ++z) {
+      float u = 0, w = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u = fmaf(s[z][j], kn[j], u);
+        w = fmaf(s[z][j], qn[j], w);
+      }
+      u = row_sum16(u);
+      w = row_sum16(w);
+      const float d = bt * (vt[z] - alpha * (u * rk)), dk = d * rk;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[z][j] = fmaf(dk, kn[j], alpha * s[z][j]);
+      if (c0 == 0 && row0 + 16 * z < a.dv)
+        a.o[(static_cast<size_t>(t) * a.Hv + h) * a.dv + row0 + 16 * z] = fmaf(dk * rq, kq, alpha * (w * rq));
+    }
   }
-  *reinterpret_cast<float4*>(srow) = *reinterpret_cast<const float4*>(s);
-  *reinterpret_cast<float4*>(srow + 4) = *reinterpret_cast<const float4*>(s + 4);
+#pragma unroll
+  for (int z = 0; z < NS; ++z) {
+    if (row0 + 16 * z < a.dv) {
+      *reinterpret_cast<float4*>(srow[z]) = *reinterpret_cast<const float4*>(s[z]);
+      *reinterpret_cast<float4*>(srow[z] + 4) = *reinterpret_cast<const float4*>(s[z] + 4);
+    }
+  }
+}
+
+// Every sequence token by token (calls of at most kShort tokens in all): one
+// workgroup per (16 state rows, value head, sequence).
+template <int ACT>
+__global__ __launch_bounds__(256) void k_gdn_tokens(GdnArgs a) {
+  const int slices = a.dv / 16;
+  int t0, t1;
+  seq_range(a, blockIdx.y, t0, t1);
+  if (t0 < t1)
+    run_tokens<ACT, 1>(a, blockIdx.y, blockIdx.x / slices, t0, t1, (blockIdx.x % slices) * 16 + (threadIdx.x >> 4));
+}
+
+// ---- in blocks of 64 tokens -------------------------------------------------
+// Within a block, with G_t the running sum of g, S the state before it and
+// k^, q^ the normalised rows, the rule is
+//   (I + A) D = beta (V - e^G K^ S^T),    A_ij = beta_i e^(G_i - G_j) k^_i.k^_j  (j < i)
+//   O = e^G Q^ S^T + P D,                 P_ij = e^(G_i - G_j) q^_i.k^_j         (j <= i)
+//   S <- e^(G_last) S + D^T (e^(G_last - G) K^).
+// k_gdn_blocks forms, for all blocks at once, what does not depend on S:
+// T = (I + A)^-1 diag(beta) and M = P T, so that with R = V - e^G K^ S^T
+//   D = T R,  O = e^G Q^ S^T + M R.
+// k_gdn_scan then takes one sequence's blocks in order.
+//
+// State and results are fp32, so fp32 operands enter the matrix cores as an
+// fp16 pair hi + lo (22 significant bits) under a power-of-two scale that
+// keeps them within fp16's range; keys and queries are exact in fp16 once each
+// row is scaled by a power of two (the row's norm is applied afterwards).
+// An operand pair costs two products against an exact operand and three
+// against another pair; fp32 matrix instructions take 8 times as long as
+// fp16's for the same product.
+constexpr int kBlock = 64;         // tokens of a block
+constexpr int kShort = 16;         // sequences up to this length go token by token
+constexpr int kRow = 136;          // LDS row of 128 fp16 values, padded
+constexpr int kRowF = 68;          // the same bytes as fp32 values
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// Workspace.  A sequence's block c sits in slot begin/64 + b + c: distinct
+// for all blocks (a sequence of n tokens takes at most ceil(n/64) <= the
+// distance to the next sequence's first slot), below n_tokens/64 + batch.
+// Operand tiles ("frags") are stored as the matrix instruction takes them, 16
+// bytes per lane.  The summed index of a 32-wide step runs, for lane group q =
+// lane/16, over 4q..4q+3 and 16+4q..16+4q+3: the order in which the result
+// tiles of two 16-row products hold their rows, so results become operands
+// without moving between lanes.
+//   per (slot, key head):   K rows [4 tiles][4 steps], Q rows the same, K columns [8 tiles][2 steps]
+//   per (slot, value head): T and M rows as [6][hi, lo] (tile rows 0, 1: step 0; 2, 3: steps 0 and 1),
+//                           256 floats: e^G rk, e^G, rq per token, then kSc*
+constexpr size_t kKeyBytes = 48 * 1024;
+constexpr size_t kHeadBytes = 25 * 1024;
+constexpr int kScGamma = 192, kScInvT = 193, kScInvM = 194, kScGmax = 195, kScD0 = 196, kScD1 = 197, kScS0 = 198,
+              kScS1 = 199;
+
+__host__ __device__ inline size_t prefill_slots(int B, int N) { return static_cast<size_t>(N) / kBlock + B; }
+
+// offset of the value heads' part, behind the key heads'
+__device__ __forceinline__ size_t prefill_ws_heads(const GdnArgs& a) {
+  return prefill_slots(a.B, a.N) * a.Hk * kKeyBytes;
+}
+
+__device__ __forceinline__ f32x4 mfma(f16x8 a, f16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f16x8 as_frag(uint4 v) { return __builtin_bit_cast(f16x8, v); }
+
+// Power of two that brings a magnitude into [2^12, 2^13), and its inverse.
+struct Pow2 {
+  float up, down;
+};
+__device__ __forceinline__ Pow2 pow2_scale(float m) {
+  const int f = min(266 - static_cast<int>((__float_as_uint(m) >> 23) & 255u), 253);
+  return {__uint_as_float(static_cast<uint32_t>(f) << 23), __uint_as_float(static_cast<uint32_t>(254 - f) << 23)};
+}
+// fp16 pair of v: hi = nearest fp16, lo = nearest fp16 of the exact rest
+__device__ __forceinline__ void split16(float v, _Float16& hi, _Float16& lo) {
+  hi = static_cast<_Float16>(v);
+  lo = static_cast<_Float16>(v - static_cast<float>(hi));
+}
+// max and sum over the four lanes that share a column (lane % 16)
+__device__ __forceinline__ float col_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16, kWave));
+  return fmaxf(v, __shfl_xor(v, 32, kWave));
+}
+__device__ __forceinline__ float col_sum(float v) {
+  v += __shfl_xor(v, 16, kWave);
+  return v + __shfl_xor(v, 32, kWave);
+}
+__device__ __forceinline__ double scan_f64(double v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double o = __shfl_up(v, d, kWave);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+// Sequence and block of a slot: the sequence is the last one whose first slot
+// (off/64 + b, increasing in b) is not above it.  64 candidates per step.
+__device__ __forceinline__ bool find_block(const GdnArgs& a, int slot, int lane, int& b, int& t0, int& len) {
+  int lo = 0, hi = a.B;
+  while (true) {
+    const int step = (hi - lo + 63) / 64, at = lo + lane * step;
+    const bool below = at < hi && min(max(a.off[min(at, a.B - 1)], 0), a.N) / kBlock + at <= slot;
+    const unsigned long long m = ~__ballot(below);
+    const int n = m == 0 ? 64 : __ffsll(m) - 1;   // candidates from the front that are not above the slot
+    if (n == 0) return false;
+    lo += (n - 1) * step;
+    hi = min(hi, lo + step);
+    if (step == 1) break;
+  }
+  b = lo;
+  int begin, end;
+  seq_range(a, b, begin, end);
+  t0 = begin + (slot - (begin / kBlock + b)) * kBlock;
+  len = min(end - t0, kBlock);
+  return len > 0 && end - begin > kShort;
+}
+
+// 16x16x16 product in fp32: acc += X Y with X rows from LDS (x: lane's row,
+// columns 4q .. 4q+3) and Y as a result tile (lane: column lane%16, rows 4q+r)
+__device__ __forceinline__ f32x4 mul16(float4 x, f32x4 y, f32x4 acc) {
+  acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x.x, y[0], acc, 0, 0, 0);
+  acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x.y, y[1], acc, 0, 0, 0);
+  acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x.z, y[2], acc, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(x.w, y[3], acc, 0, 0, 0);
+}
+
+// One workgroup per (slot, value head); wave w owns tile row w of the 64 x 64
+// products k.k and q.k, then tile column w of T and M.  The inverse is by
+// forward substitution (16 x 16 diagonal blocks column by column, then block
+// by block), which stays accurate also where powers of A grow.
+template <int ACT>
+__global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restrict__ ws) {
+  __shared__ __attribute__((aligned(16))) uint16_t ks[kBlock * kRow];
+  __shared__ __attribute__((aligned(16))) uint16_t qs[kBlock * kRow];
+  __shared__ double Gs[kBlock];
+  __shared__ float bs[kBlock], rks[kBlock], rqs[kBlock];
+  __shared__ float wmax[4][2];
+  float* As = reinterpret_cast<float*>(ks);   // takes the place of the keys once their products are done
+  float* Ps = reinterpret_cast<float*>(qs);
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, q = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int slot = blockIdx.x, h = blockIdx.y, rep = a.Hv / a.Hk, hk = h / rep;
+  int b, tok0, len;
+  if (!find_block(a, slot, lane, b, tok0, len)) return;   // the same for every thread
+
+  {   // rows of K and Q: four lanes per token, 32 columns each
+    const int row = tid >> 2, part = tid & 3;
+    const bool ok = row < len;
+    const size_t at = (static_cast<size_t>(tok0 + min(row, len - 1)) * a.Hk + hk) * kDK + 32 * part;
+    uint4 raw[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      raw[0][i] = *reinterpret_cast<const uint4*>(a.k + at + 8 * i);
+      raw[1][i] = *reinterpret_cast<const uint4*>(a.q + at + 8 * i);
+    }
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      float f[32], ss = 0.0f, mx = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const uint4& r = raw[m][i >> 3];
+        const uint32_t word = (i & 7) < 2 ? r.x : (i & 7) < 4 ? r.y : (i & 7) < 6 ? r.z : r.w;
+        f[i] = ok ? act_to_f32<ACT>((word >> (16 * (i & 1))) & 0xFFFFu) : 0.0f;
+        ss = fmaf(f[i], f[i], ss);
+        mx = fmaxf(mx, fabsf(f[i]));
+      }
+      ss += __uint_as_float(dpp_u32<0xB1>(__float_as_uint(ss)));
+      ss += __uint_as_float(dpp_u32<0x4E>(__float_as_uint(ss)));
+      mx = fmaxf(mx, __uint_as_float(dpp_u32<0xB1>(__float_as_uint(mx))));
+      mx = fmaxf(mx, __uint_as_float(dpp_u32<0x4E>(__float_as_uint(mx))));
+      const Pow2 p = pow2_scale(mx);
+      const float norm = (m ? a.q_scale : 1.0f) / sqrtf(ss + kEps);
+      if (part == 0) (m ? rqs : rks)[row] = ok ? norm * p.down : 0.0f;
+      uint16_t* dst = (m ? qs : ks) + row * kRow + 32 * part;
+#pragma unroll
+      for (int i = 0; i < 32; i += 8) {
+        f16x8 v;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = static_cast<_Float16>(f[i + j] * p.up);
+        *reinterpret_cast<f16x8*>(dst + i) = v;
+      }
+    }
+  }
+  float* vec = reinterpret_cast<float*>(ws + prefill_ws_heads(a) + (static_cast<size_t>(slot) * a.Hv + h) * kHeadBytes +
+                                        24 * 1024);
+  if (w == 0) {
+    // log decays are summed in fp64: differences of sums far from 0 keep their
+    // digits (a block of strong decays reaches -1000 and below).  -inf counts
+    // as -1000, which clears the state just as well (e^-1000 = 0 in fp32).
+    const size_t at = static_cast<size_t>(tok0 + min(lane, len - 1)) * a.Hv + h;
+    const bool ok = lane < len;
+    float gt = ok ? a.g[at] : 0.0f;
+    gt = gt < -1000.0f ? -1000.0f : gt;
+    const float bt = ok ? a.beta[at] : 0.0f;
+    const double G = scan_f64(static_cast<double>(gt), lane);
+    Gs[lane] = G;
+    bs[lane] = bt;
+    const double last = __shfl(G, 63, kWave);
+    const float eg = expf(static_cast<float>(G)), left = expf(static_cast<float>(last - G));
+    // bounds on what the block makes of a state row of norm s and values up to
+    // v (per state row), for the scales of the pairs: |R| <= v + gmax s,
+    // |e^(G_last - G) rk D| <= d0 v + d1 s, |S'| <= s0 v + s1 s.  The factors
+    // I - beta k k^T have norm max(1, |1 - beta|), rk <= 2^-12 (rows are scaled
+    // to a largest value of 2^12 or more).  With beta in [0, 2] and g <= 0,
+    // rho = rmax = 1 and gmax <= 1.
+    const float gmax = wave_max(eg), bmax = wave_max(fabsf(bt));
+    float rho = fmaxf(1.0f, fabsf(1.0f - bt));
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) rho *= __shfl_xor(rho, d, kWave);
+    const float up = wave_max(static_cast<float>(G)), dn = -wave_max(-static_cast<float>(G));
+    const float rmax = __ballot(gt > 0.0f) ? expf(fmaxf(up, 0.0f) - fminf(dn, 0.0f)) : 1.0f;
+    const float sb = wave_sum(fabsf(bt)) * rmax, sg = wave_sum(fabsf(bt) * left);
+    const float dd = bmax * rmax * 0x1p-12f;
+    if (lane == 0) {
+      vec[kScGamma] = expf(static_cast<float>(last));
+      vec[kScGmax] = gmax;
+      vec[kScD0] = dd * (1.0f + rho * sb);
+      vec[kScD1] = dd * rho * gmax;
+      vec[kScS0] = rho * sg;
+      vec[kScS1] = rho * expf(static_cast<float>(last));
+    }
+  }
+  __syncthreads();
+  if (w == 0) {
+    const float eg = expf(static_cast<float>(Gs[lane]));
+    vec[lane] = eg * rks[lane];
+    vec[64 + lane] = eg;
+    vec[128 + lane] = rqs[lane];
+  }
+  if (h % rep == 0) {   // the key head's operands, once
+    uint4* out = reinterpret_cast<uint4*>(ws + (static_cast<size_t>(slot) * a.Hk + hk) * kKeyBytes);
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      const uint16_t* src = (m ? qs : ks) + (16 * w + n) * kRow + 4 * q;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const uint2 lo = *reinterpret_cast<const uint2*>(src + 32 * s), hi = *reinterpret_cast<const uint2*>(src + 32 * s + 16);
+        out[((m * 4 + w) * 4 + s) * 64 + lane] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      }
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {   // column tiles 2w, 2w + 1 x two steps of tokens
+      const uint16_t* src = ks + 16 * (2 * w + (f >> 1)) + n + (32 * (f & 1) + 4 * q) * kRow;
+      uint32_t v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int t = (j >> 1) * 16 + 2 * (j & 1);
+        v[j] = src[t * kRow] | (static_cast<uint32_t>(src[(t + 1) * kRow]) << 16);
+      }
+      out[(32 + 4 * w + f) * 64 + lane] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+  f32x4 kk[4], qk[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    kk[j] = qk[j] = f32x4{0, 0, 0, 0};
+    if (j <= w) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const f16x8 ka = *reinterpret_cast<const f16x8*>(ks + (16 * w + n) * kRow + 32 * s + 8 * q);
+        const f16x8 qa = *reinterpret_cast<const f16x8*>(qs + (16 * w + n) * kRow + 32 * s + 8 * q);
+        const f16x8 kb = *reinterpret_cast<const f16x8*>(ks + (16 * j + n) * kRow + 32 * s + 8 * q);
+        kk[j] = mfma(ka, kb, kk[j]);
+        qk[j] = mfma(qa, kb, qk[j]);
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (j <= w) {
+      const int c = 16 * j + n;
+      const double Gc = Gs[c];
+      const float rc = rks[c];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * w + 4 * q + r;
+        const float e = expf(static_cast<float>(Gs[t] - Gc)) * rc;
+        As[t * kRowF + c] = c < t ? bs[t] * rks[t] * e * kk[j][r] : 0.0f;
+        Ps[t * kRowF + c] = c <= t ? e * qk[j][r] : 0.0f;
+      }
+    }
+  }
+  __syncthreads();
+  // column n of the inverse of diagonal block w (the four lane groups alike)
+  f32x4 tcol[4];
+  {
+    float x[16];
+    const float* blk = As + 16 * w * kRowF + 16 * w;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float v = i == n ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) v = fmaf(-blk[i * kRowF + j], x[j], v);
+      x[i] = v;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) tcol[0][r] = q == 0 ? x[r] : q == 1 ? x[4 + r] : q == 2 ? x[8 + r] : x[12 + r];
+  }
+  __syncthreads();   // the block is read by its own wave alone, but let every wave finish first
+#pragma unroll
+  for (int r = 0; r < 4; ++r) As[(16 * w + 4 * q + r) * kRowF + 16 * w + n] = tcol[0][r];
+  __syncthreads();
+  auto rows = [&](const float* m, int i, int k) {   // operand rows of block (i, k)
+    return *reinterpret_cast<const float4*>(m + (16 * i + n) * kRowF + 16 * k + 4 * q);
+  };
+#pragma unroll
+  for (int d = 1; d < 4; ++d) {
+    tcol[d] = f32x4{0, 0, 0, 0};
+    if (w + d < 4) {
+      f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < d; ++e) acc = mul16(rows(As, w + d, w + e), tcol[e], acc);
+      const f32x4 t = mul16(rows(As, w + d, w + d), acc, f32x4{0, 0, 0, 0});
+      tcol[d] = -t;
+    }
+  }
+  f32x4 mcol[4];
+  float tm = 0.0f, mm = 0.0f;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    mcol[d] = f32x4{0, 0, 0, 0};
+    if (w + d < 4) {
+#pragma unroll
+      for (int e = 0; e <= d; ++e) mcol[d] = mul16(rows(Ps, w + d, w + e), tcol[e], mcol[d]);
+    }
+  }
+  const float bc = bs[16 * w + n];
+  const double last = Gs[63];
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    if (w + d < 4) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = 16 * (w + d) + 4 * q + r;
+        tcol[d][r] *= bc * (expf(static_cast<float>(last - Gs[t])) * rks[t]);
+        mcol[d][r] *= bc;
+        // a non-finite query row must not set the scale of the others
+        const float at = fabsf(tcol[d][r]), am = fabsf(mcol[d][r]);
+        tm = fmaxf(tm, at <= 3e38f ? at : 0.0f);
+        mm = fmaxf(mm, am <= 3e38f ? am : 0.0f);
+      }
+    }
+  }
+  tm = wave_max(tm);
+  mm = wave_max(mm);
+  if (lane == 0) {
+    wmax[w][0] = tm;
+    wmax[w][1] = mm;
+  }
+  __syncthreads();
+  const Pow2 pt = pow2_scale(fmaxf(fmaxf(wmax[0][0], wmax[1][0]), fmaxf(wmax[2][0], wmax[3][0])));
+  const Pow2 pm = pow2_scale(fmaxf(fmaxf(wmax[0][1], wmax[1][1]), fmaxf(wmax[2][1], wmax[3][1])));
+  if (tid == 0) {
+    vec[kScInvT] = pt.down;
+    vec[kScInvM] = pm.down;
+  }
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    if (w + d < 4) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int at = (16 * (w + d) + 4 * q + r) * kRowF + 16 * w + n;
+        As[at] = tcol[d][r] * pt.up;
+        Ps[at] = mcol[d][r] * pm.up;
+      }
+    }
+  }
+  if (w & 1) {   // blocks (0, 1) and (2, 3) lie above the diagonal, inside a stored step
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int at = (16 * (w - 1) + 4 * q + r) * kRowF + 16 * w + n;
+      As[at] = 0.0f;
+      Ps[at] = 0.0f;
+    }
+  }
+  __syncthreads();
+  uint8_t* hd = ws + prefill_ws_heads(a) + (static_cast<size_t>(slot) * a.Hv + h) * kHeadBytes;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (s <= (w >> 1)) {
+      const int f = w < 2 ? w : 2 * w - 2 + s;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        const float* src = (m ? Ps : As) + (16 * w + n) * kRowF + 32 * s + 4 * q;
+        const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 16);
+        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        f16x8 hi, lo;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          _Float16 vh, vl;
+          split16(v[j], vh, vl);
+          hi[j] = vh;
+          lo[j] = vl;
+        }
+        f16x8* out = reinterpret_cast<f16x8*>(hd + m * 12 * 1024 + f * 2048) + lane;
+        out[0] = hi;
+        out[64] = lo;
+      }
+    }
+  }
+}
+
+// One workgroup per (sequence, value head, 16 NS state rows), its sequence's
+// blocks in order.  Wave w holds key columns 32w .. 32w+31 of the state rows
+// (result tiles: lane's column = state row) and forms tile row w of R, D and O:
+//   S pair -> LDS | R, Q S^T from all of S | R pair -> LDS | D, O from all of R
+//   | D pair -> LDS | S from all of D.
+// Three barriers a block; each operand is loaded for the next block as soon as
+// this block is done with it.
+template <int ACT, int NS>
+__global__ __launch_bounds__(256) void k_gdn_scan(GdnArgs a, const uint8_t* __restrict__ ws) {
+  __shared__ f16x8 sf[NS][4][2][64];
+  __shared__ f16x4 rf[NS][2][2][64][2];
+  __shared__ f16x4 df[NS][2][2][64][2];
+  __shared__ float2 nv[NS][4][16];   // per wave and state row: sum of squares (scaled), largest value
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, q = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // a sequence's workgroups are dealt to the eight dies in runs, so that the
+  // workgroups that read one key head's operands share an L2
+  const int slices = (a.dv + 16 * NS - 1) / (16 * NS), units = a.Hv * slices, run = (units + 7) / 8;
+  const int b = blockIdx.x / (8 * run), i = blockIdx.x % (8 * run);
+  const int unit = (i % 8) * run + i / 8;
+  if (unit >= units) return;
+  const int h = unit / slices, dv0 = (unit % slices) * 16 * NS;
+  int t0, t1;
+  seq_range(a, b, t0, t1);
+  if (t0 == t1) return;
+  if (t1 - t0 <= kShort) {
+    run_tokens<ACT, NS>(a, b, h, t0, t1, dv0 + (tid >> 4));
+    return;
+  }
+  const int nblk = (t1 - t0 + kBlock - 1) / kBlock, slot0 = t0 / kBlock + b, hk = h / (a.Hv / a.Hk);
+  const uint4* kp = reinterpret_cast<const uint4*>(ws + (static_cast<size_t>(slot0) * a.Hk + hk) * kKeyBytes) + lane;
+  const uint8_t* hp = ws + prefill_ws_heads(a) + (static_cast<size_t>(slot0) * a.Hv + h) * kHeadBytes;
+  const size_t kstep = a.Hk * kKeyBytes / 16, hstep = a.Hv * kHeadBytes;
+
+  f32x4 S[NS][2];
+  float* sp[NS];
+#pragma unroll
+  for (int z = 0; z < NS; ++z) {
+    const int row = min(dv0 + 16 * z + n, a.dv - 1);
+    sp[z] = a.state + ((static_cast<size_t>(b) * a.Hv + h) * a.dv + row) * kDK + 32 * w + 4 * q;
+    S[z][0] = *reinterpret_cast<const f32x4*>(sp[z]);
+    S[z][1] = *reinterpret_cast<const f32x4*>(sp[z] + 16);
+  }
+  uint4 kf[4], qf[4], kt[4], th[2], tl[2], mh[2], ml[2];
+  uint32_t vv[NS][4];
+  float4 av, ev, rv;
+  auto load_rows = [&](const uint4* p) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      kf[s] = p[(w * 4 + s) * 64];
+      qf[s] = p[(16 + w * 4 + s) * 64];
+    }
+  };
+  auto load_cols = [&](const uint4* p) {
+#pragma unroll
+    for (int f = 0; f < 4; ++f) kt[f] = p[(32 + 4 * w + f) * 64];
+  };
+  auto load_tm = [&](const uint8_t* p) {
+    const uint4* t = reinterpret_cast<const uint4*>(p + (w < 2 ? w : 2 * w - 2) * 2048) + lane;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (s <= (w >> 1)) {
+        th[s] = t[s * 128];
+        tl[s] = t[s * 128 + 64];
+        mh[s] = t[768 + s * 128];
+        ml[s] = t[768 + s * 128 + 64];
+      }
+    }
+  };
+  auto load_vec = [&](const uint8_t* p, int c) {
+    const float4* f = reinterpret_cast<const float4*>(p + 24 * 1024) + 4 * w + q;
+    av = f[0];
+    ev = f[16];
+    rv = f[32];
+#pragma unroll
+    for (int z = 0; z < NS; ++z)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = t0 + c * kBlock + 16 * w + 4 * q + r;
+        const uint32_t x =
+            a.v[(static_cast<size_t>(min(t, t1 - 1)) * a.Hv + h) * a.dv + min(dv0 + 16 * z + n, a.dv - 1)];
+        vv[z][r] = t < t1 ? x : 0u;
+      }
+  };
+  load_rows(kp);
+  load_tm(hp);
+  load_vec(hp, 0);
+  load_cols(kp);
+
+  float sbound[NS];   // bound on the magnitudes of the lane's state row
+#pragma unroll
+  for (int z = 0; z < NS; ++z) {
+    float m = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) m = fmaxf(m, fmaxf(fabsf(S[z][0][r]), fabsf(S[z][1][r])));
+    m = col_max(m);
+    if (q == 0) nv[z][w][n].x = m;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int z = 0; z < NS; ++z)
+    sbound[z] = fmaxf(fmaxf(nv[z][0][n].x, nv[z][1][n].x), fmaxf(nv[z][2][n].x, nv[z][3][n].x));
+  __syncthreads();
+
+  for (int c = 0; c < nblk; ++c) {
+    const bool more = c + 1 < nblk;
+    const uint4* kn = more ? kp + kstep : kp;
+    const uint8_t* hn = more ? hp + hstep : hp;
+    const float* sc = reinterpret_cast<const float*>(hp + 24 * 1024);
+    const float gamma = sc[kScGamma], inv_t = sc[kScInvT], inv_m = sc[kScInvM], gmax = sc[kScGmax], cd0 = sc[kScD0],
+                cd1 = sc[kScD1], cs0 = sc[kScS0], cs1 = sc[kScS1];
+    float inv_s[NS];
+#pragma unroll
+    for (int z = 0; z < NS; ++z) {
+      const Pow2 p = pow2_scale(sbound[z]);
+      inv_s[z] = p.down;
+      f16x8 hi, lo;
+      float ss = 0.0f, vm = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = S[z][j >> 2][j & 3] * p.up;   // scaled: its square cannot overflow
+        ss = fmaf(x, x, ss);
+        _Float16 vh, vl;
+        split16(x, vh, vl);
+        hi[j] = vh;
+        lo[j] = vl;
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) vm = fmaxf(vm, fabsf(act_to_f32<ACT>(vv[z][r])));
+      sf[z][w][0][lane] = hi;
+      sf[z][w][1][lane] = lo;
+      ss = col_sum(ss);
+      vm = col_max(vm);
+      if (q == 0) nv[z][w][n] = make_float2(ss, vm);
+    }
+    __syncthreads();
+    f32x4 X[NS], Y[NS];
+    float inv_r[NS], up_d[NS], inv_d[NS];
+#pragma unroll
+    for (int z = 0; z < NS; ++z) {
+      X[z] = Y[z] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        const f16x8 hi = sf[z][s][0][lane], lo = sf[z][s][1][lane];
+        X[z] = mfma(as_frag(kf[s]), hi, X[z]);
+        Y[z] = mfma(as_frag(qf[s]), hi, Y[z]);
+        X[z] = mfma(as_frag(kf[s]), lo, X[z]);
+        Y[z] = mfma(as_frag(qf[s]), lo, Y[z]);
+      }
+      float ss = 0.0f, vm = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 e = nv[z][u][n];
+        ss += e.x;
+        vm = fmaxf(vm, e.y);
+      }
+      const float sn = sqrtf(ss) * inv_s[z];
+      const Pow2 pr = pow2_scale(fmaf(gmax, sn, vm)), pd = pow2_scale(fmaf(cd1, sn, cd0 * vm));
+      sbound[z] = fmaf(cs1, sn, cs0 * vm);
+      inv_r[z] = pr.down;
+      up_d[z] = pd.up;
+      inv_d[z] = pd.down;
+      const float at[4] = {av.x, av.y, av.z, av.w};
+      f16x4 rh, rl;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float R = fmaf(-at[r], X[z][r] * inv_s[z], act_to_f32<ACT>(vv[z][r]));
+        _Float16 vh, vl;
+        split16(R * pr.up, vh, vl);
+        rh[r] = vh;
+        rl[r] = vl;
+      }
+      rf[z][w >> 1][0][lane][w & 1] = rh;
+      rf[z][w >> 1][1][lane][w & 1] = rl;
+    }
+    load_rows(kn);
+    __syncthreads();
+#pragma unroll
+    for (int z = 0; z < NS; ++z) {
+      f32x4 D = {0, 0, 0, 0}, O = {0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (s <= (w >> 1)) {
+          const f16x8 rh = *reinterpret_cast<const f16x8*>(&rf[z][s][0][lane][0]);
+          const f16x8 rl = *reinterpret_cast<const f16x8*>(&rf[z][s][1][lane][0]);
+          D = mfma(as_frag(th[s]), rh, D);
+          O = mfma(as_frag(mh[s]), rh, O);
+          D = mfma(as_frag(th[s]), rl, D);
+          O = mfma(as_frag(mh[s]), rl, O);
+          D = mfma(as_frag(tl[s]), rh, D);
+          O = mfma(as_frag(ml[s]), rh, O);
+        }
+      }
+      const float fd = inv_t * inv_r[z] * up_d[z], fo = inv_m * inv_r[z];
+      f16x4 dh, dl;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        _Float16 vh, vl;
+        split16(D[r] * fd, vh, vl);
+        dh[r] = vh;
+        dl[r] = vl;
+      }
+      df[z][w >> 1][0][lane][w & 1] = dh;
+      df[z][w >> 1][1][lane][w & 1] = dl;
+      const float et[4] = {ev.x, ev.y, ev.z, ev.w}, rt[4] = {rv.x, rv.y, rv.z, rv.w};
+      const int row = dv0 + 16 * z + n;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = t0 + c * kBlock + 16 * w + 4 * q + r;
+        if (t < t1 && row < a.dv)
+          a.o[(static_cast<size_t>(t) * a.Hv + h) * a.dv + row] = rt[r] * fmaf(et[r] * inv_s[z], Y[z][r], fo * O[r]);
+      }
+    }
+    load_tm(hn);
+    load_vec(hn, more ? c + 1 : c);
+    __syncthreads();
+#pragma unroll
+    for (int z = 0; z < NS; ++z) {
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        f32x4 u = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const f16x8 dh = *reinterpret_cast<const f16x8*>(&df[z][s][0][lane][0]);
+          const f16x8 dl = *reinterpret_cast<const f16x8*>(&df[z][s][1][lane][0]);
+          u = mfma(as_frag(kt[2 * m + s]), dh, u);
+          u = mfma(as_frag(kt[2 * m + s]), dl, u);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[z][m][r] = fmaf(inv_d[z], u[r], gamma * S[z][m][r]);
+      }
+    }
+    load_cols(kn);
+    kp = kn;
+    hp = hn;
+  }
+#pragma unroll
+  for (int z = 0; z < NS; ++z) {
+    if (dv0 + 16 * z + n < a.dv) {
+      *reinterpret_cast<f32x4*>(sp[z]) = S[z][0];
+      *reinterpret_cast<f32x4*>(sp[z] + 16) = S[z][1];
+    }
+  }
+}
+
+size_t prefill_bytes(const moe_gdn_desc* d, int N) {
+  return N <= kShort ? 256
+                     : prefill_slots(d->batch, N) * (d->k_heads * kKeyBytes + d->v_heads * kHeadBytes);
+}
+
+template <int ACT>
+hipError_t launch_prefill(const GdnArgs& a, uint8_t* ws, hipStream_t s) {
+  if (a.N <= kShort) {
+    hipLaunchKernelGGL(k_gdn_tokens<ACT>, dim3(a.Hv * (a.dv / 16), a.B), dim3(256), 0, s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(k_gdn_blocks<ACT>, dim3(static_cast<uint32_t>(prefill_slots(a.B, a.N)), a.Hv), dim3(256), 0, s, a,
+                     ws);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int ns = 2;
+  const int units = a.Hv * ((a.dv + 16 * ns - 1) / (16 * ns)), run = (units + 7) / 8;
+  hipLaunchKernelGGL((k_gdn_scan<ACT, 2>), dim3(static_cast<uint32_t>(a.B) * 8 * run), dim3(256), 0, s, a, ws);
+  return hipGetLastError();
 }
 
 moe_status check_prefill(const moe_gdn_desc* d, int32_t N) {
@@ -108,7 +797,7 @@ extern "C" moe_status moe_gdn_prefill_workspace_bytes(const moe_gdn_desc* d, int
   const moe_status st = moe::check_prefill(d, n_tokens);
   if (st) return st;
   if (!bytes) return moe::set_error(MOE_EINVAL, "bytes is NULL");
-  *bytes = 256;
+  *bytes = moe::prefill_bytes(d, n_tokens);
   return moe::set_error(MOE_OK, "");
 }
 
@@ -125,18 +814,15 @@ extern "C" moe_status moe_gdn_prefill(const moe_gdn_desc* d, const int32_t* seq_
     return set_error(MOE_EINVAL, "q, k and state must be 16-byte and v 2-byte aligned");
   if (!gp_aligned(seq_off, 4) || !gp_aligned(g, 4) || !gp_aligned(beta, 4) || !gp_aligned(o, 4))
     return set_error(MOE_EINVAL, "seq_off, g, beta and o must be 4-byte aligned");
-  size_t need = 0;
-  moe_gdn_prefill_workspace_bytes(d, n_tokens, &need);
+  const size_t need = moe::prefill_bytes(d, n_tokens);
   if (!ws || !gp_aligned(ws, 256)) return set_error(MOE_EINVAL, "workspace must be a 256-byte aligned device pointer");
   if (ws_bytes < need) return set_error(MOE_EWORKSPACE, "workspace of %zu bytes < required %zu", ws_bytes, need);
   moe::GdnArgs a{seq_off, static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k),
                  static_cast<const uint16_t*>(v), g, beta, state, o, q_scale, d->batch, n_tokens, d->k_heads,
                  d->v_heads, d->head_v_dim};
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-  const dim3 grid(d->v_heads * (d->head_v_dim / 16), d->batch);
-  if (d->act_dtype == MOE_BF16) hipLaunchKernelGGL(moe::k_gdn_tokens<2>, grid, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL(moe::k_gdn_tokens<1>, grid, dim3(256), 0, s, a);
-  const hipError_t e = hipGetLastError();
+  const hipError_t e = d->act_dtype == MOE_BF16 ? moe::launch_prefill<MOE_BF16>(a, static_cast<uint8_t*>(ws), s)
+                                                : moe::launch_prefill<MOE_F16>(a, static_cast<uint8_t*>(ws), s);
   if (e != hipSuccess) return set_error(MOE_EHIP, "Gated DeltaNet prefill kernel launch: %s", hipGetErrorString(e));
   return set_error(MOE_OK, "");
 }

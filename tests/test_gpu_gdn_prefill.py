@@ -222,11 +222,13 @@ def test_nonfinite_values_stay_in_their_sequence():
         assert np.array_equal(o[sl], clean[0][sl])
     assert np.array_equal(S[[0, 2]], clean[1][[0, 2]]) and not np.isfinite(S[1]).all()
     # a non-finite query only reaches its own output
-    d = inputs(lens, 1, 2, 32, "bf16", 61)
-    d["q"][76] = float("nan")
-    o, S = gpu(d, lens, "bf16")
-    keep = np.arange(141) != 76
-    assert np.isnan(o[76]).all() and np.array_equal(o[keep], clean[0][keep]) and np.array_equal(S, clean[1])
+    for bad in ("nan", "inf"):
+        d = inputs(lens, 1, 2, 32, "bf16", 61)
+        d["q"][76, 0, 5] = float(bad)
+        o, S = gpu(d, lens, "bf16")
+        keep = np.arange(141) != 76
+        assert np.array_equal(o[keep], clean[0][keep]) and np.array_equal(S, clean[1])
+        assert bad == "inf" or np.isnan(o[76]).all()
 
 
 @pytest.mark.parametrize("lens", [[5], [200, 30]], ids=["short", "blocks"])
