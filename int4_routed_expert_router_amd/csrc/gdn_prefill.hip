@@ -184,14 +184,20 @@ __device__ __forceinline__ void split16(float v, _Float16& hi, _Float16& lo) {
   hi = static_cast<_Float16>(v);
   lo = static_cast<_Float16>(v - static_cast<float>(hi));
 }
-// max and sum over the four lanes that share a column (lane % 16)
+// max and sum over the four lanes that share a column (lane % 16): swaps of
+// rows of 16 lanes and of halves
+template <class Op>
+__device__ __forceinline__ float col_reduce(float v, Op op) {
+  const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = op(__uint_as_float(x[0]), __uint_as_float(x[1]));
+  const auto y = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return op(__uint_as_float(y[0]), __uint_as_float(y[1]));
+}
 __device__ __forceinline__ float col_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, kWave));
-  return fmaxf(v, __shfl_xor(v, 32, kWave));
+  return col_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ __forceinline__ float col_sum(float v) {
-  v += __shfl_xor(v, 16, kWave);
-  return v + __shfl_xor(v, 32, kWave);
+  return col_reduce(v, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ double scan_f64(double v, int lane) {
 #pragma unroll
@@ -513,16 +519,20 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
 // One workgroup per (sequence, value head, 16 NS state rows), its sequence's
 // blocks in order.  Wave w holds key columns 32w .. 32w+31 of the state rows
 // (result tiles: lane's column = state row) and forms tile row w of R, D and O:
-//   S pair -> LDS | R, Q S^T from all of S | R pair -> LDS | D, O from all of R
-//   | D pair -> LDS | S from all of D.
-// Three barriers a block; each operand is loaded for the next block as soon as
-// this block is done with it.
+//   S pair -> LDS | K S^T, R pair -> LDS | T R = D pair -> LDS | S += D^T K.
+// Each bar is a barrier, and what is not on this chain (Q S^T, M R, bounds,
+// stores) stands where the wave would wait for LDS.  A block's operands are
+// loaded as soon as the block before is done with theirs; loads return in
+// order, so the values, which are needed first, are loaded two blocks ahead.
+// One wave per SIMD is enough work only for long batches; the chain of a
+// single sequence is bound by its latency (LDS exchanges, dependent products).
 template <int ACT, int NS>
-__global__ __launch_bounds__(256) void k_gdn_scan(GdnArgs a, const uint8_t* __restrict__ ws) {
+__global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* __restrict__ ws) {
   __shared__ f16x8 sf[NS][4][2][64];
   __shared__ f16x4 rf[NS][2][2][64][2];
   __shared__ f16x4 df[NS][2][2][64][2];
-  __shared__ float2 nv[NS][4][16];   // per wave and state row: sum of squares (scaled), largest value
+  __shared__ float ssum[NS][4][16];   // per wave and state row: sum of squares of the scaled state
+  __shared__ float vmax[NS][4][16];   // per wave and state row: largest value of the next block
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   // a sequence's workgroups are dealt to the eight dies in runs, so that the
@@ -539,10 +549,23 @@ __global__ __launch_bounds__(256) void k_gdn_scan(GdnArgs a, const uint8_t* __re
     run_tokens<ACT, NS>(a, b, h, t0, t1, dv0 + (tid >> 4));
     return;
   }
+  t0 = __builtin_amdgcn_readfirstlane(t0);
+  t1 = __builtin_amdgcn_readfirstlane(t1);
   const int nblk = (t1 - t0 + kBlock - 1) / kBlock, slot0 = t0 / kBlock + b, hk = h / (a.Hv / a.Hk);
-  const uint4* kp = reinterpret_cast<const uint4*>(ws + (static_cast<size_t>(slot0) * a.Hk + hk) * kKeyBytes) + lane;
+  const uint8_t* kp = ws + (static_cast<size_t>(slot0) * a.Hk + hk) * kKeyBytes;
   const uint8_t* hp = ws + prefill_ws_heads(a) + (static_cast<size_t>(slot0) * a.Hv + h) * kHeadBytes;
-  const size_t kstep = a.Hk * kKeyBytes / 16, hstep = a.Hv * kHeadBytes;
+  const size_t kstep = a.Hk * kKeyBytes, hstep = a.Hv * kHeadBytes;
+  // uniform bases and 32-bit lane offsets: rows 16w + 4q + r of a block
+  const uint32_t row_el = static_cast<uint32_t>(a.Hv) * a.dv;
+  const uint16_t* vbase = a.v + (static_cast<size_t>(t0 + 16 * w) * a.Hv + h) * a.dv;
+  float* obase = a.o + (static_cast<size_t>(t0 + 16 * w) * a.Hv + h) * a.dv;
+  uint32_t el[NS];   // element of row 4q, state row of the lane (a valid one for rows past the last)
+  bool row_ok[NS];
+#pragma unroll
+  for (int z = 0; z < NS; ++z) {
+    row_ok[z] = dv0 + 16 * z < a.dv;   // uniform: d_v is a multiple of 16
+    el[z] = 4u * q * row_el + min(dv0 + 16 * z + n, a.dv - 1);
+  }
 
   f32x4 S[NS][2];
   float* sp[NS];
@@ -554,201 +577,321 @@ __global__ __launch_bounds__(256) void k_gdn_scan(GdnArgs a, const uint8_t* __re
     S[z][1] = *reinterpret_cast<const f32x4*>(sp[z] + 16);
   }
   uint4 kf[4], qf[4], kt[4], th[2], tl[2], mh[2], ml[2];
-  uint32_t vv[NS][4];
-  float4 av, ev, rv;
-  auto load_rows = [&](const uint4* p) {
+  uint16_t va[NS][4], vb[NS][4];   // values of even and odd blocks
+  float4 ev, rv;
+  struct Scalars {
+    float4 a, b;   // kScGamma .. kScGmax, kScD0 .. kScS1
+    float4 eg;     // e^G rk of the lane's rows
+  } sc0, sc1;      // of even and odd blocks
+  const uint32_t lane16 = lane * 16;
+  // an offset of 0 that the compiler takes for a lane's own: the scalars come
+  // by vector loads, since a scalar load in flight makes every LDS wait wait for it
+  uint32_t zero = 0;
+  asm volatile("" : "+v"(zero));
+  auto frag = [&](const uint8_t* p, uint32_t at) { return *reinterpret_cast<const uint4*>(p + (lane16 + at)); };
+  auto vec4 = [&](const uint8_t* p, uint32_t at) {
+    return *reinterpret_cast<const float4*>(p + (24 * 1024 + 64 * w + 16u * q + at));
+  };
+  auto load_scalars = [&](const uint8_t* ph, Scalars& sc) {
+    sc.a = *reinterpret_cast<const float4*>(ph + (24 * 1024 + 4 * kScGamma + zero));
+    sc.b = *reinterpret_cast<const float4*>(ph + (24 * 1024 + 4 * kScD0 + zero));
+    sc.eg = vec4(ph, 0);
+  };
+  auto load_keys = [&](const uint8_t* pk) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      kf[s] = p[(w * 4 + s) * 64];
-      qf[s] = p[(16 + w * 4 + s) * 64];
+    for (int s = 0; s < 4; ++s) kf[s] = frag(pk + w * 4096, 1024 * s);
+  };
+  auto load_queries = [&](const uint8_t* pk) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) qf[s] = frag(pk + 16384 + w * 4096, 1024 * s);
+  };
+  auto load_t = [&](const uint8_t* ph) {
+    const uint8_t* p = ph + (w < 2 ? w : 2 * w - 2) * 2048;
+    th[0] = frag(p, 0);
+    tl[0] = frag(p, 1024);
+    if (w >= 2) {
+      th[1] = frag(p, 2048);
+      tl[1] = frag(p, 3072);
     }
   };
-  auto load_cols = [&](const uint4* p) {
-#pragma unroll
-    for (int f = 0; f < 4; ++f) kt[f] = p[(32 + 4 * w + f) * 64];
+  auto load_m = [&](const uint8_t* ph) {
+    const uint8_t* p = ph + 12288 + (w < 2 ? w : 2 * w - 2) * 2048;
+    mh[0] = frag(p, 0);
+    ml[0] = frag(p, 1024);
+    if (w >= 2) {
+      mh[1] = frag(p, 2048);
+      ml[1] = frag(p, 3072);
+    }
+    ev = vec4(ph, 256);
+    rv = vec4(ph, 512);
   };
-  auto load_tm = [&](const uint8_t* p) {
-    const uint4* t = reinterpret_cast<const uint4*>(p + (w < 2 ? w : 2 * w - 2) * 2048) + lane;
+  auto load_cols = [&](const uint8_t* pk) {
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (s <= (w >> 1)) {
-        th[s] = t[s * 128];
-        tl[s] = t[s * 128 + 64];
-        mh[s] = t[768 + s * 128];
-        ml[s] = t[768 + s * 128 + 64];
-      }
+    for (int f = 0; f < 4; ++f) kt[f] = frag(pk + 32768 + w * 4096, 1024 * f);
+  };
+  auto load_values = [&](int c, uint16_t (&vv)[NS][4]) {
+    const uint16_t* p = vbase + static_cast<size_t>(c) * kBlock * row_el;
+    if (t0 + (c + 1) * kBlock <= t1) {   // uniform
+#pragma unroll
+      for (int z = 0; z < NS; ++z)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) vv[z][r] = *(p + r * row_el + el[z]);
+    } else {   // rows past the end repeat the sequence's last token (masked at use)
+#pragma unroll
+      for (int z = 0; z < NS; ++z)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = min(t0 + c * kBlock + 16 * w + 4 * q + r, t1 - 1);
+          vv[z][r] = a.v[(static_cast<size_t>(t) * a.Hv + h) * a.dv + min(dv0 + 16 * z + n, a.dv - 1)];
+        }
     }
   };
-  auto load_vec = [&](const uint8_t* p, int c) {
-    const float4* f = reinterpret_cast<const float4*>(p + 24 * 1024) + 4 * w + q;
-    av = f[0];
-    ev = f[16];
-    rv = f[32];
+  // masks the block's values and leaves their largest magnitude in LDS
+  auto prepare_values = [&](int c, uint16_t (&vv)[NS][4]) {
+    const int left = t1 - (t0 + c * kBlock + 16 * w);   // uniform
 #pragma unroll
-    for (int z = 0; z < NS; ++z)
+    for (int z = 0; z < NS; ++z) {
+      float m = 0.0f;
+      if (left < 16) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = t0 + c * kBlock + 16 * w + 4 * q + r;
-        const uint32_t x =
-            a.v[(static_cast<size_t>(min(t, t1 - 1)) * a.Hv + h) * a.dv + min(dv0 + 16 * z + n, a.dv - 1)];
-        vv[z][r] = t < t1 ? x : 0u;
+        for (int r = 0; r < 4; ++r) vv[z][r] = 4 * q + r < left ? vv[z][r] : 0;
       }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(act_to_f32<ACT>(vv[z][r])));
+      vmax[z][w][n] = col_max(m);   // the same from the four lanes of a column
+    }
   };
-  load_rows(kp);
-  load_tm(hp);
-  load_vec(hp, 0);
+  load_values(0, va);
+  load_scalars(hp, sc0);
+  load_keys(kp);
+  load_queries(kp);
+  load_t(hp);
+  load_m(hp);
   load_cols(kp);
+  load_values(1, vb);
 
-  float sbound[NS];   // bound on the magnitudes of the lane's state row
+  // bound[z]: on the norm of the lane's state row (exact at first)
+  float bound[NS];
 #pragma unroll
   for (int z = 0; z < NS; ++z) {
     float m = 0.0f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) m = fmaxf(m, fmaxf(fabsf(S[z][0][r]), fabsf(S[z][1][r])));
-    m = col_max(m);
-    if (q == 0) nv[z][w][n].x = m;
+    ssum[z][w][n] = col_max(m);
   }
+  prepare_values(0, va);
   __syncthreads();
 #pragma unroll
-  for (int z = 0; z < NS; ++z)
-    sbound[z] = fmaxf(fmaxf(nv[z][0][n].x, nv[z][1][n].x), fmaxf(nv[z][2][n].x, nv[z][3][n].x));
+  for (int z = 0; z < NS; ++z)   // 128 elements: norm <= 11.4 times the largest
+    bound[z] = 11.4f * fmaxf(fmaxf(ssum[z][0][n], ssum[z][1][n]), fmaxf(ssum[z][2][n], ssum[z][3][n]));
   __syncthreads();
 
-  for (int c = 0; c < nblk; ++c) {
+  auto block = [&](int c, uint16_t (&vv)[NS][4], uint16_t (&vnext)[NS][4], const Scalars& sc, Scalars& scnext) {
     const bool more = c + 1 < nblk;
-    const uint4* kn = more ? kp + kstep : kp;
+    const uint8_t* kn = more ? kp + kstep : kp;
     const uint8_t* hn = more ? hp + hstep : hp;
-    const float* sc = reinterpret_cast<const float*>(hp + 24 * 1024);
-    const float gamma = sc[kScGamma], inv_t = sc[kScInvT], inv_m = sc[kScInvM], gmax = sc[kScGmax], cd0 = sc[kScD0],
-                cd1 = sc[kScD1], cs0 = sc[kScS0], cs1 = sc[kScS1];
-    float inv_s[NS];
+    load_scalars(hn, scnext);
+    const float gamma = sc.a.x, inv_t = sc.a.y, inv_m = sc.a.z, gmax = sc.a.w, cd0 = sc.b.x, cd1 = sc.b.y,
+                cs0 = sc.b.z, cs1 = sc.b.w;
+    float inv_s[NS], fd[NS], fo[NS], inv_d[NS], vs[NS][4], as[NS][4];
+    // S pair
 #pragma unroll
     for (int z = 0; z < NS; ++z) {
-      const Pow2 p = pow2_scale(sbound[z]);
+      const Pow2 p = pow2_scale(bound[z]);
       inv_s[z] = p.down;
       f16x8 hi, lo;
-      float ss = 0.0f, vm = 0.0f;
+      float ss = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float x = S[z][j >> 2][j & 3] * p.up;   // scaled: its square cannot overflow
-        ss = fmaf(x, x, ss);
         _Float16 vh, vl;
         split16(x, vh, vl);
         hi[j] = vh;
         lo[j] = vl;
+        ss = fmaf(x, x, ss);
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) vm = fmaxf(vm, fabsf(act_to_f32<ACT>(vv[z][r])));
       sf[z][w][0][lane] = hi;
       sf[z][w][1][lane] = lo;
-      ss = col_sum(ss);
-      vm = col_max(vm);
-      if (q == 0) nv[z][w][n] = make_float2(ss, vm);
+      ssum[z][w][n] = col_sum(ss);
     }
-    __syncthreads();
-    f32x4 X[NS], Y[NS];
-    float inv_r[NS], up_d[NS], inv_d[NS];
+    // scales of R and D from the bounds; V and e^G rk under R's scale
 #pragma unroll
     for (int z = 0; z < NS; ++z) {
-      X[z] = Y[z] = f32x4{0, 0, 0, 0};
+      const float vm = fmaxf(fmaxf(vmax[z][0][n], vmax[z][1][n]), fmaxf(vmax[z][2][n], vmax[z][3][n]));
+      const Pow2 pr = pow2_scale(fmaf(gmax, bound[z], vm)), pd = pow2_scale(fmaf(cd1, bound[z], cd0 * vm));
+      fd[z] = inv_t * pr.down * pd.up;
+      fo[z] = inv_m * pr.down;
+      inv_d[z] = pd.down;
+      bound[z] = cs0 * vm;   // the next block's, completed below
+      const float at[4] = {sc.eg.x, sc.eg.y, sc.eg.z, sc.eg.w};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        vs[z][r] = act_to_f32<ACT>(vv[z][r]) * pr.up;
+        as[z][r] = at[r] * (inv_s[z] * pr.up);
+      }
+    }
+    __syncthreads();
+    // K S^T and the R pair
+    f16x8 sh[NS][4], sl[NS][4];
+    f32x4 X[NS][2];
+#pragma unroll
+    for (int z = 0; z < NS; ++z) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) {
-        const f16x8 hi = sf[z][s][0][lane], lo = sf[z][s][1][lane];
-        X[z] = mfma(as_frag(kf[s]), hi, X[z]);
-        Y[z] = mfma(as_frag(qf[s]), hi, Y[z]);
-        X[z] = mfma(as_frag(kf[s]), lo, X[z]);
-        Y[z] = mfma(as_frag(qf[s]), lo, Y[z]);
+        sh[z][s] = sf[z][s][0][lane];
+        sl[z][s] = sf[z][s][1][lane];
       }
-      float ss = 0.0f, vm = 0.0f;
+    }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float2 e = nv[z][u][n];
-        ss += e.x;
-        vm = fmaxf(vm, e.y);
+    for (int z = 0; z < NS; ++z) X[z][0] = X[z][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int z = 0; z < NS; ++z) {
+        X[z][0] = mfma(as_frag(kf[s]), sh[z][s], X[z][0]);
+        X[z][1] = mfma(as_frag(kf[s]), sl[z][s], X[z][1]);
       }
-      const float sn = sqrtf(ss) * inv_s[z];
-      const Pow2 pr = pow2_scale(fmaf(gmax, sn, vm)), pd = pow2_scale(fmaf(cd1, sn, cd0 * vm));
-      sbound[z] = fmaf(cs1, sn, cs0 * vm);
-      inv_r[z] = pr.down;
-      up_d[z] = pd.up;
-      inv_d[z] = pd.down;
-      const float at[4] = {av.x, av.y, av.z, av.w};
+    }
+#pragma unroll
+    for (int z = 0; z < NS; ++z) {
       f16x4 rh, rl;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float R = fmaf(-at[r], X[z][r] * inv_s[z], act_to_f32<ACT>(vv[z][r]));
         _Float16 vh, vl;
-        split16(R * pr.up, vh, vl);
+        split16(fmaf(-as[z][r], X[z][0][r] + X[z][1][r], vs[z][r]), vh, vl);
         rh[r] = vh;
         rl[r] = vl;
       }
       rf[z][w >> 1][0][lane][w & 1] = rh;
       rf[z][w >> 1][1][lane][w & 1] = rl;
     }
-    load_rows(kn);
+    load_keys(kn);
     __syncthreads();
+    // T R and the D pair; Q S^T meanwhile
+    f16x8 rh[NS][2], rl[NS][2];
 #pragma unroll
     for (int z = 0; z < NS; ++z) {
-      f32x4 D = {0, 0, 0, 0}, O = {0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         if (s <= (w >> 1)) {
-          const f16x8 rh = *reinterpret_cast<const f16x8*>(&rf[z][s][0][lane][0]);
-          const f16x8 rl = *reinterpret_cast<const f16x8*>(&rf[z][s][1][lane][0]);
-          D = mfma(as_frag(th[s]), rh, D);
-          O = mfma(as_frag(mh[s]), rh, O);
-          D = mfma(as_frag(th[s]), rl, D);
-          O = mfma(as_frag(mh[s]), rl, O);
-          D = mfma(as_frag(tl[s]), rh, D);
-          O = mfma(as_frag(ml[s]), rh, O);
+          rh[z][s] = *reinterpret_cast<const f16x8*>(&rf[z][s][0][lane][0]);
+          rl[z][s] = *reinterpret_cast<const f16x8*>(&rf[z][s][1][lane][0]);
         }
       }
-      const float fd = inv_t * inv_r[z] * up_d[z], fo = inv_m * inv_r[z];
+    }
+    f32x4 Y[NS];
+#pragma unroll
+    for (int z = 0; z < NS; ++z) Y[z] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int z = 0; z < NS; ++z) {
+        Y[z] = mfma(as_frag(qf[s]), sh[z][s], Y[z]);
+        Y[z] = mfma(as_frag(qf[s]), sl[z][s], Y[z]);
+      }
+    }
+#pragma unroll
+    for (int z = 0; z < NS; ++z) {
+      f32x4 D0 = {0, 0, 0, 0}, D1 = {0, 0, 0, 0};
+      D0 = mfma(as_frag(th[0]), rh[z][0], D0);
+      D1 = mfma(as_frag(tl[0]), rh[z][0], D1);
+      D0 = mfma(as_frag(th[0]), rl[z][0], D0);
+      if (w >= 2) {
+        D1 = mfma(as_frag(tl[1]), rh[z][1], D1);
+        D0 = mfma(as_frag(th[1]), rh[z][1], D0);
+        D1 = mfma(as_frag(th[1]), rl[z][1], D1);
+      }
       f16x4 dh, dl;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         _Float16 vh, vl;
-        split16(D[r] * fd, vh, vl);
+        split16((D0[r] + D1[r]) * fd[z], vh, vl);
         dh[r] = vh;
         dl[r] = vl;
       }
       df[z][w >> 1][0][lane][w & 1] = dh;
       df[z][w >> 1][1][lane][w & 1] = dl;
-      const float et[4] = {ev.x, ev.y, ev.z, ev.w}, rt[4] = {rv.x, rv.y, rv.z, rv.w};
-      const int row = dv0 + 16 * z + n;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = t0 + c * kBlock + 16 * w + 4 * q + r;
-        if (t < t1 && row < a.dv)
-          a.o[(static_cast<size_t>(t) * a.Hv + h) * a.dv + row] = rt[r] * fmaf(et[r] * inv_s[z], Y[z][r], fo * O[r]);
-      }
     }
-    load_tm(hn);
-    load_vec(hn, more ? c + 1 : c);
+#pragma unroll
+    for (int z = 0; z < NS; ++z) {
+      const float ss = (ssum[z][0][n] + ssum[z][1][n]) + (ssum[z][2][n] + ssum[z][3][n]);
+      bound[z] = fmaf(cs1 * inv_s[z], __builtin_amdgcn_sqrtf(ss), bound[z]);
+    }
+    load_queries(kn);
+    load_t(hn);
+    if (more) prepare_values(c + 1, vnext);
     __syncthreads();
+    // the new state; M R and the output meanwhile
+    f16x8 dh[NS][2], dl[NS][2];
 #pragma unroll
     for (int z = 0; z < NS; ++z) {
 #pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        dh[z][s] = *reinterpret_cast<const f16x8*>(&df[z][s][0][lane][0]);
+        dl[z][s] = *reinterpret_cast<const f16x8*>(&df[z][s][1][lane][0]);
+      }
+    }
+    f32x4 O[NS];
+#pragma unroll
+    for (int z = 0; z < NS; ++z) {
+      O[z] = mfma(as_frag(ml[0]), rh[z][0], f32x4{0, 0, 0, 0});
+      O[z] = mfma(as_frag(mh[0]), rl[z][0], O[z]);
+      O[z] = mfma(as_frag(mh[0]), rh[z][0], O[z]);
+      if (w >= 2) {
+        O[z] = mfma(as_frag(ml[1]), rh[z][1], O[z]);
+        O[z] = mfma(as_frag(mh[1]), rl[z][1], O[z]);
+        O[z] = mfma(as_frag(mh[1]), rh[z][1], O[z]);
+      }
+    }
+#pragma unroll
+    for (int z = 0; z < NS; ++z) {
+      f32x4 u[2];
+#pragma unroll
       for (int m = 0; m < 2; ++m) {
-        f32x4 u = {0, 0, 0, 0};
+        u[m] = mfma(as_frag(kt[2 * m]), dh[z][0], f32x4{0, 0, 0, 0});
+        u[m] = mfma(as_frag(kt[2 * m]), dl[z][0], u[m]);
+        u[m] = mfma(as_frag(kt[2 * m + 1]), dh[z][1], u[m]);
+        u[m] = mfma(as_frag(kt[2 * m + 1]), dl[z][1], u[m]);
+      }
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const f16x8 dh = *reinterpret_cast<const f16x8*>(&df[z][s][0][lane][0]);
-          const f16x8 dl = *reinterpret_cast<const f16x8*>(&df[z][s][1][lane][0]);
-          u = mfma(as_frag(kt[2 * m + s]), dh, u);
-          u = mfma(as_frag(kt[2 * m + s]), dl, u);
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[z][m][r] = fmaf(inv_d[z], u[m][r], gamma * S[z][m][r]);
+    }
+    const float et[4] = {ev.x, ev.y, ev.z, ev.w}, rt[4] = {rv.x, rv.y, rv.z, rv.w};
+    float* op = obase + static_cast<size_t>(c) * kBlock * row_el;
+    const int left = t1 - (t0 + c * kBlock + 16 * w);   // uniform
+#pragma unroll
+    for (int z = 0; z < NS; ++z) {
+      if (row_ok[z]) {
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = rt[r] * fmaf(et[r] * inv_s[z], Y[z][r], fo[z] * O[z][r]);
+        if (left >= 16) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) *(op + r * row_el + el[z]) = v[r];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if (4 * q + r < left) *(op + r * row_el + el[z]) = v[r];
         }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) S[z][m][r] = fmaf(inv_d[z], u[r], gamma * S[z][m][r]);
       }
     }
     load_cols(kn);
+    load_m(hn);
+    load_values(c + 2, vv);
     kp = kn;
     hp = hn;
+  };
+  for (int c = 0;;) {
+    block(c, va, vb, sc0, sc1);
+    if (++c == nblk) break;
+    block(c, vb, va, sc1, sc0);
+    if (++c == nblk) break;
   }
 #pragma unroll
   for (int z = 0; z < NS; ++z) {
-    if (dv0 + 16 * z + n < a.dv) {
+    if (row_ok[z]) {
       *reinterpret_cast<f32x4*>(sp[z]) = S[z][0];
       *reinterpret_cast<f32x4*>(sp[z] + 16) = S[z][1];
     }
@@ -770,9 +913,12 @@ hipError_t launch_prefill(const GdnArgs& a, uint8_t* ws, hipStream_t s) {
                      ws);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int ns = 2;
+  // 16 state rows per workgroup: with 32 the compiler keeps a block's operands
+  // in more registers than two waves per SIMD leave (516 against 325 us at 8192
+  // tokens with one wave per SIMD, 1270 us with spills)
+  constexpr int ns = 1;
   const int units = a.Hv * ((a.dv + 16 * ns - 1) / (16 * ns)), run = (units + 7) / 8;
-  hipLaunchKernelGGL((k_gdn_scan<ACT, 2>), dim3(static_cast<uint32_t>(a.B) * 8 * run), dim3(256), 0, s, a, ws);
+  hipLaunchKernelGGL((k_gdn_scan<ACT, ns>), dim3(static_cast<uint32_t>(a.B) * 8 * run), dim3(256), 0, s, a, ws);
   return hipGetLastError();
 }
 
