@@ -74,12 +74,17 @@ __global__ __launch_bounds__(64 * kLinWaves) void k_linear(const uint8_t* __rest
   for (int tt = 0; tt < TT; ++tt) acc[tt][0] = acc[tt][1] = f32x4{0, 0, 0, 0};
   const uint4 ones = ones_operand<ACT>();
   for (int c0 = wave; c0 < nc; c0 += kLinWaves * kLinBatch) {
-    uint4 w[kLinBatch];
+    uint4 w[kLinBatch], xv[kLinBatch][TT][2];
     ScaleBias sb[kLinBatch][G32 ? 2 : 1];
 #pragma unroll
     for (int u = 0; u < kLinBatch; ++u) {
       const int c = min(c0 + u * kLinWaves, nc - 1);
       w[u] = wq[static_cast<size_t>(c) * 64];
+#pragma unroll
+      for (int tt = 0; tt < TT; ++tt) {
+        xv[u][tt][0] = *reinterpret_cast<const uint4*>(xr[tt] + 64 * c);
+        xv[u][tt][1] = *reinterpret_cast<const uint4*>(xr[tt] + 64 * c + 32);
+      }
       if constexpr (G32) {
         sb[u][0] = load_sb(sec, p, ng, 2 * c, n);
         sb[u][1] = load_sb(sec, p, ng, 2 * c + 1, n);
@@ -99,11 +104,10 @@ __global__ __launch_bounds__(64 * kLinWaves) void k_linear(const uint8_t* __rest
         const bool fresh = G32 || ks == 0;
 #pragma unroll
         for (int tt = 0; tt < TT; ++tt) {
-          const uint4 xv = *reinterpret_cast<const uint4*>(xr[tt] + 64 * c + 32 * ks);
           const f32x4 zero = {0, 0, 0, 0};
-          ga[tt] = mfma32<ACT>(xv, va, fresh ? zero : ga[tt]);
-          gb[tt] = mfma32<ACT>(xv, vb, fresh ? zero : gb[tt]);
-          gx[tt] = mfma32<ACT>(xv, ones, fresh ? zero : gx[tt]);
+          ga[tt] = mfma32<ACT>(xv[u][tt][ks], va, fresh ? zero : ga[tt]);
+          gb[tt] = mfma32<ACT>(xv[u][tt][ks], vb, fresh ? zero : gb[tt]);
+          gx[tt] = mfma32<ACT>(xv[u][tt][ks], ones, fresh ? zero : gx[tt]);
         }
         if (G32 || ks == 1) {
           const ScaleBias s = sb[u][G32 ? ks : 0];
@@ -132,6 +136,148 @@ __global__ __launch_bounds__(64 * kLinWaves) void k_linear(const uint8_t* __rest
     const int col = 32 * p + 16 * ((r >> 2) & 1) + n;
     if (t < T && col < N) store_out<RES>(y, static_cast<size_t>(t) * N + col, v);
   }
+}
+
+// Prompts: one workgroup of 8 waves per 128 tokens x 128 weight rows; wave
+// (th, p) has tokens 64 th .. 64 th + 63 and pair-tile p.  Per 64-column chunk
+// the tokens' values are staged in LDS (two buffers, one barrier a chunk; the
+// 16-byte pieces of a row are xor-swizzled by the row so that the operand
+// reads spread over the banks) and each wave converts its own weights.  The
+// staging threads also leave each token's sums over units of 64 columns (32
+// with groups of 32) in LDS; every 4 units the (b - 16 s) (sum x) term is
+// added by fp32 matrix instructions (4 units deep), which costs a quarter of
+// the main products' matrix time and spares 32 multiply-adds a chunk.
+constexpr int kTileT = 128, kTileN = 128;
+template <int ACT, int RES, bool G32>
+__global__ __launch_bounds__(512, 2) void k_linear_tile(const uint8_t* __restrict__ packed,
+                                                        const uint16_t* __restrict__ x, void* __restrict__ y, int T,
+                                                        int N, int K, int G, uint64_t scale_off) {
+  constexpr int kUnits = G32 ? 2 : 1;             // units per chunk
+  __shared__ uint4 xs[2][kTileT * 8];             // [token][8 pieces of 16 bytes]
+  __shared__ float sums[2][kTileT][5];            // [4 units' buffer][token][unit], padded
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), th = wave >> 2;
+  // the token tiles of one row tile run on the same die, one after the other
+  const int nt = (T + kTileT - 1) / kTileT, id = blockIdx.x / 8;
+  const int r0 = ((id / nt) * 8 + blockIdx.x % 8) * (kTileN / 32), tok0 = (id % nt) * kTileT;
+  const int np = (N + 31) / 32, nc = K / 64, ng = K / G;
+  if (r0 >= np) return;   // the grid is a multiple of 8 row tiles
+  const int p = r0 + (wave & 3);
+  const bool rows = p < np;   // uniform; a wave without rows still stages
+  const int pc = min(p, np - 1);
+  const uint4* wq = reinterpret_cast<const uint4*>(packed + static_cast<uint64_t>(pc) * nc * 1024) + lane;
+  const uint8_t* sec = packed + scale_off;
+  // staging: thread's two pieces of tokens tid/8 and tid/8 + 64
+  const int st = tid >> 3, sp = tid & 7;
+  const uint16_t* xsrc[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    xsrc[i] = x + static_cast<size_t>(min(tok0 + st + 64 * i, T - 1)) * K + 8 * sp;
+  auto unit_group = [&](int u) { return G32 ? u : (G == 128 ? u >> 1 : u); };
+  uint4 xr[2], w0, w1;
+  ScaleBias s0[kUnits], s1[kUnits];
+  auto load_x = [&](int c) {
+    const int cc = min(c, nc - 1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) xr[i] = *reinterpret_cast<const uint4*>(xsrc[i] + 64 * cc);
+  };
+  auto load_w = [&](int c, uint4& w, ScaleBias (&sb)[kUnits]) {
+    const int cc = min(c, nc - 1);
+    w = wq[static_cast<size_t>(cc) * 64];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) sb[u] = load_sb(sec, pc, ng, unit_group(cc * kUnits + u), n);
+  };
+  constexpr uint32_t one = ACT == 2 ? 0x3F803F80u : 0x3C003C00u;
+  auto stage = [&](int c) {   // pieces and unit sums of chunk c
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = st + 64 * i;
+      xs[c & 1][t * 8 + (sp ^ (t & 7))] = xr[i];
+      float v = dot2_acc<ACT>(xr[i].x, one, 0.0f);
+      v = dot2_acc<ACT>(xr[i].y, one, v);
+      v = dot2_acc<ACT>(xr[i].z, one, v);
+      v = dot2_acc<ACT>(xr[i].w, one, v);
+      v += __uint_as_float(dpp_u32<0xB1>(__float_as_uint(v)));
+      v += __uint_as_float(dpp_u32<0x4E>(__float_as_uint(v)));
+      if constexpr (!G32) v += __uint_as_float(dpp_u32<0x141>(__float_as_uint(v)));
+      const int u = c * kUnits + (G32 ? sp >> 2 : 0);
+      if ((sp & (G32 ? 3 : 7)) == 0) sums[(u >> 2) & 1][t][u & 3] = v;
+    }
+  };
+  f32x4 acc[4][2];
+#pragma unroll
+  for (int tt = 0; tt < 4; ++tt) acc[tt][0] = acc[tt][1] = f32x4{0, 0, 0, 0};
+  // units 4 j .. 4 j + 3 (those below `units`) of the (b - 16 s) (sum x) term
+  auto add_sums = [&](int j, int units) {
+    const int u = 4 * j + q;
+    const ScaleBias s = load_sb(sec, pc, ng, unit_group(min(u, units - 1)), n);
+    const float ba = u < units ? s.bA - 16.0f * s.sA : 0.0f, bb = u < units ? s.bB - 16.0f * s.sB : 0.0f;
+#pragma unroll
+    for (int tt = 0; tt < 4; ++tt) {
+      const float v = u < units ? sums[j & 1][64 * th + 16 * tt + n][q] : 0.0f;
+      acc[tt][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, ba, acc[tt][0], 0, 0, 0);
+      acc[tt][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, bb, acc[tt][1], 0, 0, 0);
+    }
+  };
+  auto chunk = [&](int c, uint4& w, ScaleBias (&sb)[kUnits]) {
+    // the next chunk's values are on their way; this chunk's weights were
+    // loaded two chunks ago
+    load_x(c + 1);
+    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    f32x4 g[4][2];
+    const f32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      const uint4 va = v_operand<ACT>(ww[ks]), vb = v_operand<ACT>(ww[2 + ks]);
+      const bool fresh = G32 || ks == 0;
+#pragma unroll
+      for (int tt = 0; tt < 4; ++tt) {
+        const int t = 64 * th + 16 * tt + n;
+        const uint4 xv = xs[c & 1][t * 8 + ((4 * ks + q) ^ (t & 7))];
+        g[tt][0] = mfma32<ACT>(xv, va, fresh ? zero : g[tt][0]);
+        g[tt][1] = mfma32<ACT>(xv, vb, fresh ? zero : g[tt][1]);
+      }
+      if (G32 || ks == 1) {
+        const ScaleBias s = sb[G32 ? ks : 0];
+#pragma unroll
+        for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            acc[tt][0][i] = fmaf(16.0f * s.sA, g[tt][0][i], acc[tt][0][i]);
+            acc[tt][1][i] = fmaf(16.0f * s.sB, g[tt][1][i], acc[tt][1][i]);
+          }
+      }
+    }
+    load_w(c + 2, w, sb);
+    const int done = (c + 1) * kUnits;   // units whose sums are staged and visible
+    if ((done & 3) == 0) add_sums((done >> 2) - 1, done);
+    else if (c + 1 == nc) add_sums(done >> 2, done);
+    if (c + 1 < nc) {
+      stage(c + 1);
+      __syncthreads();
+    }
+  };
+  load_x(0);
+  load_w(0, w0, s0);
+  load_w(1, w1, s1);
+  stage(0);
+  __syncthreads();
+  for (int c = 0;;) {
+    chunk(c, w0, s0);
+    if (++c == nc) break;
+    chunk(c, w1, s1);
+    if (++c == nc) break;
+  }
+  if (!rows) return;
+#pragma unroll
+  for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = tok0 + 64 * th + 16 * tt + 4 * q + i, col = 32 * p + 16 * m + n;
+        if (t < T && col < N) store_out<RES>(y, static_cast<size_t>(t) * N + col, acc[tt][m][i]);
+      }
 }
 
 // One thread per packed word (values), then one per 8-byte scale entry.
@@ -177,16 +323,23 @@ hipError_t launch_linear(const moe_linear_desc* d, const uint8_t* packed, const 
                          hipStream_t s) {
   const int K = d->in_dim, N = d->out_dim, G = d->group_size;
   const uint64_t off = padded_rows(N) * K / 2;
-  const int tt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
-  const dim3 grid((N + 31) / 32, (T + 16 * tt - 1) / (16 * tt)), block(64 * kLinWaves);
+  const int np = (N + 31) / 32, nt = (T + kTileT - 1) / kTileT, nr = (N + kTileN - 1) / kTileN;
+  if (T > 64 && static_cast<int64_t>(nt) * nr >= 128) {
+    const dim3 grid((nr + 7) / 8 * 8 * nt), block(512);
+    if (G == 32) hipLaunchKernelGGL((k_linear_tile<ACT, RES, true>), grid, block, 0, s, packed, x, y, T, N, K, G, off);
+    else hipLaunchKernelGGL((k_linear_tile<ACT, RES, false>), grid, block, 0, s, packed, x, y, T, N, K, G, off);
+    return hipGetLastError();
+  }
+  const int tiles = (T + 15) / 16;
+  const int tt = tiles == 1 || static_cast<int64_t>(np) * tiles <= 512 ? 1 : 2;
+  const dim3 grid(np, (tiles + tt - 1) / tt), block(64 * kLinWaves);
 #define LIN(TT)                                                                                             \
   do {                                                                                                      \
     if (G == 32) hipLaunchKernelGGL((k_linear<ACT, RES, TT, true>), grid, block, 0, s, packed, x, y, T, N, K, G, off); \
     else hipLaunchKernelGGL((k_linear<ACT, RES, TT, false>), grid, block, 0, s, packed, x, y, T, N, K, G, off);        \
   } while (0)
   if (tt == 1) LIN(1);
-  else if (tt == 2) LIN(2);
-  else LIN(4);
+  else LIN(2);
 #undef LIN
   return hipGetLastError();
 }

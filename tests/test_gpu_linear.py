@@ -41,6 +41,9 @@ CASES = [  # T, K, N, G, act, res
     (33, 8192, 129, 64, "bf16", "f32"), (64, 1024, 257, 128, "f16", "f32"), (65, 512, 48, 64, "bf16", "f32"),
     (127, 384, 160, 128, "bf16", "f32"), (129, 640, 130, 128, "f16", "f32"), (300, 1088, 259, 64, "bf16", "bf16"),
     (513, 2048, 385, 32, "f16", "f32"), (1000, 128, 128, 64, "bf16", "f32"),
+    # many rows: the tiles of 128 tokens x 128 rows
+    (70, 192, 16400, 64, "bf16", "f32"), (257, 64, 5600, 32, "f16", "f16"), (130, 640, 8300, 128, "f16", "f32"),
+    (385, 320, 4200, 32, "bf16", "bf16"), (128, 1152, 16385, 128, "bf16", "f32"), (65, 576, 16300, 64, "f16", "f32"),
 ]
 IDS = ["T%d_K%d_N%d_G%d_%s_%s" % c for c in CASES]
 
@@ -110,7 +113,7 @@ def test_nonfinite_tokens_reach_their_own_row_only():
     q = rng.integers(0, 16, (N, K))
     s = np.full((N, K // G), 0.01, np.float16)
     lin = make(K, N, G, "bf16", q, s, (-8 * s).astype(np.float16))
-    for T in (20, 200):
+    for T in (20, 200, 16500):
         x = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).cuda().bfloat16()
         clean = run(lin, x, "f32")
         x[7, 3], x[T - 1, 0] = float("nan"), float("inf")
@@ -120,7 +123,7 @@ def test_nonfinite_tokens_reach_their_own_row_only():
         assert np.array_equal(got[keep], clean[keep])
 
 
-@pytest.mark.parametrize("T", [1, 40, 300])
+@pytest.mark.parametrize("T", [1, 40, 300, 9000])
 def test_repeatable_captured_and_on_another_stream(T):
     import torch
     from int4_routed_expert_router_amd import api
