@@ -33,9 +33,18 @@ __device__ __forceinline__ f32x4 mfma32(uint4 a, uint4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
                                                   0);
 }
+// q_pair of all four pairs of a word: one shift and one and-or each (the
+// compiler does not form the and-or from two constants)
 template <int ACT>
 __device__ __forceinline__ uint4 v_operand(uint32_t w) {
-  return make_uint4(q_pair<ACT>(w, 0), q_pair<ACT>(w, 1), q_pair<ACT>(w, 2), q_pair<ACT>(w, 3));
+  constexpr uint32_t mask = ACT == 2 ? 0x00780078u : 0x03C003C0u, one = ACT == 2 ? 0x3F803F80u : 0x3C003C00u;
+  auto pair = [&](uint32_t t) {
+    uint32_t r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(t), "s"(mask), "v"(one));
+    return r;
+  };
+  if constexpr (ACT == 2) return make_uint4(pair(w << 3), pair(w >> 1), pair(w >> 5), pair(w >> 9));
+  else return make_uint4(pair(w << 6), pair(w << 2), pair(w >> 2), pair(w >> 6));
 }
 template <int ACT>
 __device__ __forceinline__ uint4 ones_operand() {
@@ -138,146 +147,195 @@ __global__ __launch_bounds__(64 * kLinWaves) void k_linear(const uint8_t* __rest
   }
 }
 
-// Prompts: one workgroup of 8 waves per 128 tokens x 128 weight rows; wave
-// (th, p) has tokens 64 th .. 64 th + 63 and pair-tile p.  Per 64-column chunk
-// the tokens' values are staged in LDS (two buffers, one barrier a chunk; the
-// 16-byte pieces of a row are xor-swizzled by the row so that the operand
-// reads spread over the banks) and each wave converts its own weights.  The
-// staging threads also leave each token's sums over units of 64 columns (32
-// with groups of 32) in LDS; every 4 units the (b - 16 s) (sum x) term is
-// added by fp32 matrix instructions (4 units deep), which costs a quarter of
-// the main products' matrix time and spares 32 multiply-adds a chunk.
+// Prompts: one workgroup of 8 waves per 128 tokens x 128 weight rows.  Wave
+// (g, p) has pair-tile p of the rows, all 128 tokens (no weight is converted
+// twice) and the 64-column chunks 2 i + g; the two halves are added at the end.
+// Two waves per SIMD on different chunks let one wave's conversions and
+// scalings run beside the other's matrix products.  A chunk's tokens are
+// staged in LDS (two buffers, one barrier per pair of chunks; the 16-byte
+// pieces of a row are xor-swizzled by the row so that the operand reads spread
+// over the banks).  The staging threads also leave each token's sums over
+// units of 64 columns (32 with groups of 32) in LDS; every 4 units the
+// (b - 16 s) (sum x) term is added by fp32 matrix instructions (4 units deep),
+// which costs a quarter of the main products' matrix time and spares 64
+// multiply-adds a chunk.
 constexpr int kTileT = 128, kTileN = 128;
+// v + v of the lane that the DPP control names (one instruction)
+template <int kCtrl>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __uint_as_float(static_cast<uint32_t>(
+                 __builtin_amdgcn_update_dpp(0, static_cast<int>(__float_as_uint(v)), kCtrl, 0xF, 0xF, true)));
+}
 template <int ACT, int RES, bool G32>
 __global__ __launch_bounds__(512, 2) void k_linear_tile(const uint8_t* __restrict__ packed,
                                                         const uint16_t* __restrict__ x, void* __restrict__ y, int T,
                                                         int N, int K, int G, uint64_t scale_off) {
   constexpr int kUnits = G32 ? 2 : 1;             // units per chunk
-  __shared__ uint4 xs[2][kTileT * 8];             // [token][8 pieces of 16 bytes]
-  __shared__ float sums[2][kTileT][5];            // [4 units' buffer][token][unit], padded
-  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), th = wave >> 2;
+  constexpr int kTT = kTileT / 16;
+  __shared__ uint4 xs[2][2][kTileT * 8];          // [half][buffer][token][8 pieces of 16 bytes]
+  __shared__ float sums[2][2][kTileT][5];         // [half][4 units' buffer][token][unit], padded
+  const int tid = threadIdx.x & 255, lane = tid & 63, n = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = wave >> 2;
   // the token tiles of one row tile run on the same die, one after the other
   const int nt = (T + kTileT - 1) / kTileT, id = blockIdx.x / 8;
   const int r0 = ((id / nt) * 8 + blockIdx.x % 8) * (kTileN / 32), tok0 = (id % nt) * kTileT;
   const int np = (N + 31) / 32, nc = K / 64, ng = K / G;
   if (r0 >= np) return;   // the grid is a multiple of 8 row tiles
   const int p = r0 + (wave & 3);
-  const bool rows = p < np;   // uniform; a wave without rows still stages
-  const int pc = min(p, np - 1);
-  const uint4* wq = reinterpret_cast<const uint4*>(packed + static_cast<uint64_t>(pc) * nc * 1024) + lane;
-  const uint8_t* sec = packed + scale_off;
-  // staging: thread's two pieces of tokens tid/8 and tid/8 + 64
+  const int pc = min(p, np - 1);   // a wave without rows still stages
+  const int nit = (nc + 1) / 2, mine = (nc + 1 - half) / 2;   // steps, and this half's chunks
+  const uint8_t* wq = packed + static_cast<uint64_t>(pc) * nc * 1024 + half * 1024;
+  const uint8_t* sec = packed + scale_off + static_cast<uint64_t>(pc) * ng * 128;
+  // staging: the thread's piece of tokens tid/8 + 32 i
   const int st = tid >> 3, sp = tid & 7;
-  const uint16_t* xsrc[2];
+  const uint16_t* xsrc[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    xsrc[i] = x + static_cast<size_t>(min(tok0 + st + 64 * i, T - 1)) * K + 8 * sp;
-  auto unit_group = [&](int u) { return G32 ? u : (G == 128 ? u >> 1 : u); };
-  uint4 xr[2], w0, w1;
-  ScaleBias s0[kUnits], s1[kUnits];
-  auto load_x = [&](int c) {
-    const int cc = min(c, nc - 1);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) xr[i] = *reinterpret_cast<const uint4*>(xsrc[i] + 64 * cc);
+  for (int i = 0; i < 4; ++i)
+    xsrc[i] = x + static_cast<size_t>(min(tok0 + st + 32 * i, T - 1)) * K + 64 * half + 8 * sp;
+  // group of this half's unit u (its units run over its own chunks)
+  auto group_of = [&](int u) {
+    const int c = 2 * (u / kUnits) + half;
+    return G32 ? 2 * c + (u & 1) : (G == 128 ? c >> 1 : c);
   };
-  auto load_w = [&](int c, uint4& w, ScaleBias (&sb)[kUnits]) {
-    const int cc = min(c, nc - 1);
-    w = wq[static_cast<size_t>(cc) * 64];
+  struct Loads {
+    uint4 x[4], w;
+    uint2 s[kUnits];   // [s_A, b_A, s_B, b_B] of the chunk's units
+  } even, odd;
+  auto load = [&](int i, Loads& l) {   // chunk i of this half (past the last: the last that exists)
+    const int cc = max(min(i, mine - 1), 0), back = mine > 0 ? 0 : 1;   // without any chunk: chunk 0
 #pragma unroll
-    for (int u = 0; u < kUnits; ++u) sb[u] = load_sb(sec, pc, ng, unit_group(cc * kUnits + u), n);
+    for (int m = 0; m < 4; ++m) l.x[m] = *reinterpret_cast<const uint4*>(xsrc[m] + 128 * cc - 64 * back);
+    l.w = *reinterpret_cast<const uint4*>(wq + static_cast<size_t>(cc) * 2048 - 1024 * back + 16 * lane);
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+      l.s[u] = *reinterpret_cast<const uint2*>(sec + min(group_of(cc * kUnits + u), ng - 1) * 128 + 8 * n);
   };
   constexpr uint32_t one = ACT == 2 ? 0x3F803F80u : 0x3C003C00u;
-  auto stage = [&](int c) {   // pieces and unit sums of chunk c
+  auto stage = [&](int i, const Loads& l) {   // pieces and unit sums of chunk i
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = st + 64 * i;
-      xs[c & 1][t * 8 + (sp ^ (t & 7))] = xr[i];
-      float v = dot2_acc<ACT>(xr[i].x, one, 0.0f);
-      v = dot2_acc<ACT>(xr[i].y, one, v);
-      v = dot2_acc<ACT>(xr[i].z, one, v);
-      v = dot2_acc<ACT>(xr[i].w, one, v);
-      v += __uint_as_float(dpp_u32<0xB1>(__float_as_uint(v)));
-      v += __uint_as_float(dpp_u32<0x4E>(__float_as_uint(v)));
-      if constexpr (!G32) v += __uint_as_float(dpp_u32<0x141>(__float_as_uint(v)));
-      const int u = c * kUnits + (G32 ? sp >> 2 : 0);
-      if ((sp & (G32 ? 3 : 7)) == 0) sums[(u >> 2) & 1][t][u & 3] = v;
+    for (int m = 0; m < 4; ++m) {
+      const int t = st + 32 * m;
+      xs[half][i & 1][t * 8 + (sp ^ (t & 7))] = l.x[m];
+      float v = dot2_acc<ACT>(l.x[m].x, one, 0.0f);
+      v = dot2_acc<ACT>(l.x[m].y, one, v);
+      v = dot2_acc<ACT>(l.x[m].z, one, v);
+      v = dot2_acc<ACT>(l.x[m].w, one, v);
+      v = add_dpp<0x4E>(add_dpp<0xB1>(v));
+      if constexpr (!G32) v = add_dpp<0x141>(v);
+      const int u = i * kUnits + (G32 ? sp >> 2 : 0);
+      sums[half][(u >> 2) & 1][t][u & 3] = v;   // the same from every thread of the unit
     }
   };
-  f32x4 acc[4][2];
+  f32x4 acc[kTT][2];
 #pragma unroll
-  for (int tt = 0; tt < 4; ++tt) acc[tt][0] = acc[tt][1] = f32x4{0, 0, 0, 0};
-  // units 4 j .. 4 j + 3 (those below `units`) of the (b - 16 s) (sum x) term
+  for (int tt = 0; tt < kTT; ++tt) acc[tt][0] = acc[tt][1] = f32x4{0, 0, 0, 0};
+  // units 4 j .. 4 j + 3 (those below `units`) of the (b - 16 s) (sum x) term;
+  // its scales are loaded when unit 4 j begins
+  uint2 sq = make_uint2(0, 0);
   auto add_sums = [&](int j, int units) {
-    const int u = 4 * j + q;
-    const ScaleBias s = load_sb(sec, pc, ng, unit_group(min(u, units - 1)), n);
-    const float ba = u < units ? s.bA - 16.0f * s.sA : 0.0f, bb = u < units ? s.bB - 16.0f * s.sB : 0.0f;
+    const bool on = 4 * j + q < units;
+    const float ba = on ? f16_bits_to_f32(sq.x >> 16) - 16.0f * f16_bits_to_f32(sq.x & 0xFFFFu) : 0.0f;
+    const float bb = on ? f16_bits_to_f32(sq.y >> 16) - 16.0f * f16_bits_to_f32(sq.y & 0xFFFFu) : 0.0f;
 #pragma unroll
-    for (int tt = 0; tt < 4; ++tt) {
-      const float v = u < units ? sums[j & 1][64 * th + 16 * tt + n][q] : 0.0f;
+    for (int tt = 0; tt < kTT; ++tt) {
+      float v = sums[half][j & 1][16 * tt + n][q];   // not yet written where !on
+      v = on ? v : 0.0f;
       acc[tt][0] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, ba, acc[tt][0], 0, 0, 0);
       acc[tt][1] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, bb, acc[tt][1], 0, 0, 0);
     }
   };
-  auto chunk = [&](int c, uint4& w, ScaleBias (&sb)[kUnits]) {
-    // the next chunk's values are on their way; this chunk's weights were
-    // loaded two chunks ago
-    load_x(c + 1);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-    f32x4 g[4][2];
-    const f32x4 zero = {0, 0, 0, 0};
+  // values and weights are loaded two steps ahead: a step's products take less
+  // time than a load from L2
+  auto step = [&](int i, Loads& cur, Loads& next) {
+    const uint32_t ww[4] = {cur.w.x, cur.w.y, cur.w.z, cur.w.w};
+    uint4 va[2], vb[2];
+    float sa[kUnits], sB[kUnits];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      const uint4 va = v_operand<ACT>(ww[ks]), vb = v_operand<ACT>(ww[2 + ks]);
-      const bool fresh = G32 || ks == 0;
-#pragma unroll
-      for (int tt = 0; tt < 4; ++tt) {
-        const int t = 64 * th + 16 * tt + n;
-        const uint4 xv = xs[c & 1][t * 8 + ((4 * ks + q) ^ (t & 7))];
-        g[tt][0] = mfma32<ACT>(xv, va, fresh ? zero : g[tt][0]);
-        g[tt][1] = mfma32<ACT>(xv, vb, fresh ? zero : g[tt][1]);
-      }
-      if (G32 || ks == 1) {
-        const ScaleBias s = sb[G32 ? ks : 0];
-#pragma unroll
-        for (int tt = 0; tt < 4; ++tt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            acc[tt][0][i] = fmaf(16.0f * s.sA, g[tt][0][i], acc[tt][0][i]);
-            acc[tt][1][i] = fmaf(16.0f * s.sB, g[tt][1][i], acc[tt][1][i]);
-          }
-      }
+      va[ks] = v_operand<ACT>(ww[ks]);
+      vb[ks] = v_operand<ACT>(ww[2 + ks]);
     }
-    load_w(c + 2, w, sb);
-    const int done = (c + 1) * kUnits;   // units whose sums are staged and visible
-    if ((done & 3) == 0) add_sums((done >> 2) - 1, done);
-    else if (c + 1 == nc) add_sums(done >> 2, done);
-    if (c + 1 < nc) {
-      stage(c + 1);
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      sa[u] = 16.0f * f16_bits_to_f32(cur.s[u].x & 0xFFFFu);
+      sB[u] = 16.0f * f16_bits_to_f32(cur.s[u].y & 0xFFFFu);
+    }
+    // This step's registers are free (its tokens lie in LDS).  A use of them
+    // that the compiler moved behind the loads would make it load into others
+    // and wait for them at the loop's end to copy them: opaque to it.
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      asm volatile("" : "+v"(va[ks].x), "+v"(va[ks].y), "+v"(va[ks].z), "+v"(va[ks].w));
+      asm volatile("" : "+v"(vb[ks].x), "+v"(vb[ks].y), "+v"(vb[ks].z), "+v"(vb[ks].w));
+    }
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) asm volatile("" : "+v"(sa[u]), "+v"(sB[u]));
+    __builtin_amdgcn_sched_barrier(0);
+    load(i + 2, cur);
+    if (((i * kUnits) & 3) == 0)
+      sq = *reinterpret_cast<const uint2*>(sec + min(group_of(i * kUnits + q), ng - 1) * 128 + 8 * n);
+    if (i < mine) {   // uniform: the second half may have one chunk less
+      const f32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+      for (int tt = 0; tt < kTT; ++tt) {
+        const int t = 16 * tt + n;
+        const uint4 x0 = xs[half][i & 1][t * 8 + (q ^ (t & 7))], x1 = xs[half][i & 1][t * 8 + ((4 + q) ^ (t & 7))];
+        f32x4 ga = mfma32<ACT>(x0, va[0], zero), gb = mfma32<ACT>(x0, vb[0], zero);
+        if constexpr (G32) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            acc[tt][0][r] = fmaf(sa[0], ga[r], acc[tt][0][r]);
+            acc[tt][1][r] = fmaf(sB[0], gb[r], acc[tt][1][r]);
+          }
+          ga = gb = zero;
+        }
+        ga = mfma32<ACT>(x1, va[1], ga);
+        gb = mfma32<ACT>(x1, vb[1], gb);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          acc[tt][0][r] = fmaf(sa[kUnits - 1], ga[r], acc[tt][0][r]);
+          acc[tt][1][r] = fmaf(sB[kUnits - 1], gb[r], acc[tt][1][r]);
+        }
+      }
+      const int done = (i + 1) * kUnits;   // units whose sums are staged and visible
+      if ((done & 3) == 0 || i + 1 == mine) add_sums((done - 1) >> 2, done);
+    }
+    if (i + 1 < nit) {
+      stage(i + 1, next);
       __syncthreads();
     }
   };
-  load_x(0);
-  load_w(0, w0, s0);
-  load_w(1, w1, s1);
-  stage(0);
+  load(0, even);
+  load(1, odd);
+  stage(0, even);
   __syncthreads();
-  for (int c = 0;;) {
-    chunk(c, w0, s0);
-    if (++c == nc) break;
-    chunk(c, w1, s1);
-    if (++c == nc) break;
+  // (a loop with one exit: with a second one in its middle the compiler has
+  // every step wait for the loads of the step before)
+  for (int i = 0; i + 1 < nit; i += 2) {
+    step(i, even, odd);
+    step(i + 1, odd, even);
   }
-  if (!rows) return;
+  if (nit & 1) step(nit - 1, even, odd);
+  // half g keeps tile g of the pair and hands the other one over
+  __syncthreads();
+  float* ex = reinterpret_cast<float*>(&xs[0][0][0]) + wave * (kTT * 4 * 64);   // 8 waves x 8 KB
 #pragma unroll
-  for (int tt = 0; tt < 4; ++tt)
+  for (int tt = 0; tt < kTT; ++tt)
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int r = 0; r < 4; ++r) ex[(tt * 4 + r) * 64 + lane] = half ? acc[tt][0][r] : acc[tt][1][r];
+  __syncthreads();
+  const float* other = reinterpret_cast<const float*>(&xs[0][0][0]) + (wave ^ 4) * (kTT * 4 * 64);
+  const int col = 32 * p + 16 * half + n;
+  if (p >= np || col >= N) return;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = tok0 + 64 * th + 16 * tt + 4 * q + i, col = 32 * p + 16 * m + n;
-        if (t < T && col < N) store_out<RES>(y, static_cast<size_t>(t) * N + col, acc[tt][m][i]);
-      }
+  for (int tt = 0; tt < kTT; ++tt)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int t = tok0 + 16 * tt + 4 * q + r;
+      const float o = other[(tt * 4 + r) * 64 + lane];
+      const float v = half ? o + acc[tt][1][r] : acc[tt][0][r] + o;   // even chunks' sum first
+      if (t < T) store_out<RES>(y, static_cast<size_t>(t) * N + col, v);
+    }
 }
 
 // One thread per packed word (values), then one per 8-byte scale entry.
