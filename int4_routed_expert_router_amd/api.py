@@ -26,6 +26,7 @@ __all__ = ["Desc", "Layer", "blob_bytes", "pack_expert", "workspace_bytes", "wor
 
 
 _ACT = {"bf16": MOE_BF16, "f16": MOE_F16}
+_ACTS = {"bf16": (torch.bfloat16, torch.int16), "f16": (torch.float16, torch.int16)}
 _ACT_DTYPES = (torch.int16, torch.float16, torch.bfloat16)
 
 
@@ -74,19 +75,38 @@ def _scratch(desc, T, device, stream):
     return ws
 
 
-def _device(ref, **others):
-    """Index of the device that ref and every other tensor given live on."""
-    dev = ref.device
-    for name, t in others.items():
-        if isinstance(t, torch.Tensor) and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    return dev.index
+def _arg(t, name, dtypes, numel, dev):
+    """_ptr for a call on device dev: also refuses a tensor on another device.
+    The tests are the cheap ones first; _ptr says what is wrong."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.get_device() == dev and t.is_contiguous()
+            and (dtypes is None or t.dtype in dtypes) and (numel is None or t.numel() == numel)):
+        return t.data_ptr()
+    p = _ptr(t, name, dtypes, numel)
+    if isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    return p
+
+
+def _device(t, name):
+    """Index of the GPU that a call's first tensor lives on."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch tensor, got {type(t).__name__}")
+    dev = t.get_device()
+    if dev < 0 or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    return dev
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _stream_on(dev, stream):
     """Handle of the stream (None: the current stream of device dev)."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(dev)
     if isinstance(stream, torch.cuda.Stream) and stream.device.index != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
     return _stream(stream)
@@ -95,10 +115,12 @@ def _stream_on(dev, stream):
 def _call_on(dev, fn, *args):
     """Status check of a library call made with device dev current."""
     if torch.cuda.current_device() == dev:
-        check(fn(*args))
+        status = fn(*args)
     else:
         with torch.cuda.device(dev):
-            check(fn(*args))
+            status = fn(*args)
+    if status:
+        check(status)
 
 
 def _tokens(x, desc, name="x"):
@@ -242,11 +264,11 @@ def select(desc, logits, topk_idx, topk_w, bias=None, shared_gate=None, stream=N
     T, cols = logits.shape
     if cols != E and cols != E + 1:
         raise ValueError(f"logits has {cols} columns, expected {E} or {E + 1}")
-    args = (_ptr(logits, "logits", _F32), cols, _ptr(bias, "bias", _F32, E), T,
-            _ptr(topk_idx, "topk_idx", _I32, T * K), _ptr(topk_w, "topk_w", _F32, T * K),
-            _ptr(shared_gate, "shared_gate", _F32, T))
-    dev = _device(logits, bias=bias, topk_idx=topk_idx, topk_w=topk_w, shared_gate=shared_gate)
-    _call_on(dev, lib().moe_select, desc.c(), *args, _stream_on(dev, stream))
+    dev = _device(logits, "logits")
+    _call_on(dev, lib().moe_select, desc.c(), _arg(logits, "logits", _F32, None, dev), cols,
+             _arg(bias, "bias", _F32, E, dev), T, _arg(topk_idx, "topk_idx", _I32, T * K, dev),
+             _arg(topk_w, "topk_w", _F32, T * K, dev), _arg(shared_gate, "shared_gate", _F32, T, dev),
+             _stream_on(dev, stream))
 
 
 def route_scored(desc, sel, layer, x, topk_idx, topk_w, shared_gate=None, logits=None, ws=None, stream=None):
@@ -254,14 +276,16 @@ def route_scored(desc, sel, layer, x, topk_idx, topk_w, shared_gate=None, logits
     router_bias is the balance bias.  expert_ffn() takes the outputs."""
     T = _tokens(x, desc)
     K, E = desc.top_k, desc.n_experts
-    args = (_ptr(x), T, _ptr(topk_idx, "topk_idx", _I32, T * K), _ptr(topk_w, "topk_w", _F32, T * K),
-            _ptr(shared_gate, "shared_gate", _F32, T), _ptr(logits, "logits", _F32, T * (E + 1)))
-    dev = _device(x, topk_idx=topk_idx, topk_w=topk_w, shared_gate=shared_gate, logits=logits, ws=ws,
-                  router_w=layer.router_w, router_bias=layer.router_bias)
+    dev = _device(x, "x")
+    args = (_ptr(x), T, _arg(topk_idx, "topk_idx", _I32, T * K, dev), _arg(topk_w, "topk_w", _F32, T * K, dev),
+            _arg(shared_gate, "shared_gate", _F32, T, dev), _arg(logits, "logits", _F32, T * (E + 1), dev))
+    for name, t in (("router_w", layer.router_w), ("router_bias", layer.router_bias)):
+        _arg(t, name, None, None, dev)
     d, w = desc.c(), layer.c()
-    ws = _scratch(desc, T, x.device, stream) if ws is None else ws
-    _call_on(dev, lib().moe_route_scored, C.byref(d), sel.c(), C.byref(w), *args, _ws(ws), ws.numel(),
-             _stream_on(dev, stream))
+    if ws is None:
+        ws = _scratch(desc, T, x.device, stream)
+    _call_on(dev, lib().moe_route_scored, C.byref(d), sel.c(), C.byref(w), *args,
+             _arg(ws, "ws", (torch.uint8,), None, dev), ws.numel(), _stream_on(dev, stream))
 
 
 def permute(desc, topk_idx, expert_off, perm, inv=None, ws=None, stream=None):
@@ -513,11 +537,12 @@ def gdn_prefill(q, k, v, g, beta, state, o, seq_off, q_scale, act_dtype="bf16", 
     N, Hk, dk = q.shape
     Hv, dv = v.shape[1], v.shape[2]
     B = state.shape[0]
-    acts = {"bf16": (torch.bfloat16, torch.int16), "f16": (torch.float16, torch.int16)}.get(act_dtype, _ACT_DTYPES)
-    args = (_ptr(seq_off, "seq_off", _I32, B + 1), N, _ptr(q, "q", acts), _ptr(k, "k", acts, N * Hk * dk),
-            _ptr(v, "v", acts, N * Hv * dv), _ptr(g, "g", _F32, N * Hv), _ptr(beta, "beta", _F32, N * Hv),
-            float(q_scale), _ptr(state, "state", _F32, B * Hv * dv * dk), _ptr(o, "o", _F32, N * Hv * dv))
-    dev = _device(q, k=k, v=v, g=g, beta=beta, state=state, o=o, seq_off=seq_off, ws=ws)
+    acts = _ACTS.get(act_dtype, _ACT_DTYPES)
+    dev = _device(q, "q")
+    args = (_arg(seq_off, "seq_off", _I32, B + 1, dev), N, _arg(q, "q", acts, None, dev),
+            _arg(k, "k", acts, N * Hk * dk, dev), _arg(v, "v", acts, N * Hv * dv, dev),
+            _arg(g, "g", _F32, N * Hv, dev), _arg(beta, "beta", _F32, N * Hv, dev), float(q_scale),
+            _arg(state, "state", _F32, B * Hv * dv * dk, dev), _arg(o, "o", _F32, N * Hv * dv, dev))
     d = GdnDesc(B, Hk, Hv, dk, dv, _ACT.get(act_dtype, 0))
     if ws is None:
         if stream is not None and not isinstance(stream, torch.cuda.Stream):
@@ -525,7 +550,8 @@ def gdn_prefill(q, k, v, g, beta, state, o, seq_off, q_scale, act_dtype="bf16", 
         ws = gdn_prefill_workspace(B, N, Hk, Hv, dv, act_dtype, dk, q.device)
         if stream is not None and stream != torch.cuda.current_stream(ws.device):
             ws.record_stream(stream)
-    _call_on(dev, lib().moe_gdn_prefill, C.byref(d), *args, _ws(ws), ws.numel(), _stream_on(dev, stream))
+    _call_on(dev, lib().moe_gdn_prefill, C.byref(d), *args, _arg(ws, "ws", (torch.uint8,), None, dev), ws.numel(),
+             _stream_on(dev, stream))
 
 
 _OUT = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
@@ -548,15 +574,13 @@ class Linear:
             raise ValueError(f"act_dtype {act_dtype!r} is not 'f16' or 'bf16'")
         f16 = (torch.float16, torch.int16)
         ng = out_dim * (in_dim // group_size)
-        args = (_ptr(words, "words", _I32, out_dim * in_dim // 8), _ptr(scale, "scale", f16, ng),
-                _ptr(bias, "bias", f16, ng))
-        if any(a is None for a in args):
-            raise ValueError("words, scale and bias are required")
-        dev = _device(words, scale=scale, bias=bias)
+        dev = _device(words, "words")
+        args = (_arg(words, "words", _I32, out_dim * in_dim // 8, dev), _arg(scale, "scale", f16, ng, dev),
+                _arg(bias, "bias", f16, ng, dev))
         self.in_dim, self.out_dim, self.group_size, self.act_dtype = in_dim, out_dim, group_size, act_dtype
         self.packed = torch.empty(n, dtype=torch.uint8, device=words.device)
-        act = {"bf16": MOE_BF16, "f16": MOE_F16}[act_dtype]
-        self._c = {t: LinearDesc(in_dim, out_dim, group_size, act, o) for t, o in _OUT.items()}
+        self._acts = _ACTS[act_dtype]
+        self._c = {t: LinearDesc(in_dim, out_dim, group_size, _ACT[act_dtype], o) for t, o in _OUT.items()}
         _call_on(dev, lib().moe_linear_pack, in_dim, out_dim, group_size, *args, self.packed.data_ptr(),
                  _stream_on(dev, stream))
         if isinstance(stream, torch.cuda.Stream):
@@ -571,11 +595,10 @@ def linear(lin, x, y, stream=None):
     if not isinstance(y, torch.Tensor) or y.dtype not in _OUT:
         raise ValueError("y must be a float16, bfloat16 or float32 tensor")
     T = x.shape[0]
-    act = torch.bfloat16 if lin.act_dtype == "bf16" else torch.float16
-    args = (lin.packed.data_ptr(), _ptr(x, "x", (act, torch.int16), T * lin.in_dim), T,
-            _ptr(y, "y", None, T * lin.out_dim))
-    dev = _device(x, y=y, weights=lin.packed)
-    _call_on(dev, lib().moe_linear_forward, lin._c[y.dtype], *args, _stream_on(dev, stream))
+    dev = _device(x, "x")
+    _call_on(dev, lib().moe_linear_forward, lin._c[y.dtype], _arg(lin.packed, "weights", None, None, dev),
+             _arg(x, "x", lin._acts, T * lin.in_dim, dev), T, _arg(y, "y", None, T * lin.out_dim, dev),
+             _stream_on(dev, stream))
 
 
 def synth_fill_experts(seed, layer, expert_first, n_experts, hidden, inter, group, scale_lo, scale_hi, dst, stride,

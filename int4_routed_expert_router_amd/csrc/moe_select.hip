@@ -1,9 +1,13 @@
 // Scored, biased and group-limited expert choice (see include/moe_select.h
 // for the definition).
 //
-// One wave per token.  Lane l holds experts l, l + 64, ... .  Scores and keys
-// are fp64, so the order is the true one also where two keys differ by less
-// than an fp32 rounding.
+// One wave per token.  Lane l holds experts l, l + 64, ... .  The order is that
+// of fp64 keys, but a wave first takes fp32 keys, whose error is bounded.  Its
+// rounds go on past rank K until a key is below the one before by more than the
+// bound: what came before holds the first K.  Where two of those candidates
+// are nearer than the bound, their fp64 keys (one per lane) put them in order.
+// Only where the fp32 keys leave open which groups take part, or where 64
+// candidates lie too near each other, does the wave start over in fp64.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -11,6 +15,7 @@
 #include "moe_common.h"
 #include "moe_kernels.h"
 #include "moe_select.h"
+#include "moe_topk.h"
 
 namespace moe {
 moe_status set_error(moe_status code, const char* fmt, ...);
@@ -44,81 +49,101 @@ __device__ __forceinline__ double soft_ex(float z, float m) {
   return z == m ? 1.0 : exp(static_cast<double>(z) - static_cast<double>(m));
 }
 
+// The two largest of keys g per + i, i = first, first + L, ... < per (-inf for
+// g >= n_group); four reads are in flight at a time.
+template <class F>
+__device__ __forceinline__ void two_largest(const F* keys, int per, int g, int first, int L, int n_group, F& b1, F& b2) {
+  const F ninf = -INFINITY;
+  b1 = b2 = ninf;
+  const F* mine = keys + min(g, n_group - 1) * per;
+  for (int i = first; i < per; i += 4 * L) {
+    F k[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) k[u] = mine[min(i + u * L, per - 1)];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const F v = g < n_group && i + u * L < per ? k[u] : ninf;
+      b2 = fmax(b2, fmin(b1, v));
+      b1 = fmax(b1, v);
+    }
+  }
+}
+// Groups: lanes g L .. g L + L - 1 scan group g's keys (in LDS) for its two
+// largest; every lane of group g returns its rank.
+template <class F>
+__device__ __forceinline__ F group_rank(const SelectArgs& a, const F* keys, int lane, int L) {
+  F b1, b2;
+  two_largest(keys, a.E / a.n_group, lane / L, lane % L, L, a.n_group, b1, b2);
+  const F ninf = -INFINITY;
+  for (int s = 1; s < L; s <<= 1) {
+    const F o1 = __shfl_xor(b1, s, kWave), o2 = __shfl_xor(b2, s, kWave);
+    b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+    b1 = fmax(b1, o1);
+  }
+  return a.group_top == 2 && b2 > ninf ? b1 + b2 : b1;
+}
+// Bit c: group c is kept (fewer than top_groups groups come before it).
+template <class F>
+__device__ __forceinline__ uint64_t kept_groups(const SelectArgs& a, F rank, int lane, int L) {
+  const int g = lane / L;
+  uint64_t kept = 0;
+  for (int c0 = 0; c0 < a.n_group; c0 += 4) {   // four ranks fetched at a time
+    F rc[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) rc[u] = __shfl(rank, min(c0 + u, a.n_group - 1) * L, kWave);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int c = c0 + u;
+      const bool before = lane % L == 0 && g < a.n_group && (rank > rc[u] || (rank == rc[u] && g < c));
+      if (c < a.n_group && __popcll(__ballot(before)) < a.top_groups) kept |= 1ull << c;
+    }
+  }
+  return kept;
+}
+__device__ __forceinline__ int group_of(int e, float inv_per) {   // e / per, exact for e < 1024
+  return static_cast<int>((static_cast<float>(e) + 0.5f) * inv_per);
+}
+
+struct Softmax {
+  float m;        // maximum of the logits
+  double total;   // sum of exp(z - m) over the live experts
+};
 template <int kJ>
-__device__ void select_token(const SelectArgs& a, int t, int lane, double* keys) {
+__device__ __forceinline__ double total64(const float (&z)[kJ], float m) {
+  double s = 0.0;
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) s += is_off(z[j]) ? 0.0 : soft_ex(z[j], m);
+  return wave_sum_f64(s);
+}
+__device__ __forceinline__ double score64(const SelectArgs& a, float z, const Softmax& sm) {
+  return a.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-static_cast<double>(z))) : soft_ex(z, sm.m) / sm.total;
+}
+
+// The choice in fp64: lane k returns the expert of rank k, or -1.
+template <int kJ>
+__device__ __forceinline__ int choose64(const SelectArgs& a, const float (&z)[kJ], const Softmax& sm, int lane, int L,
+                                        double* keys) {
   const double ninf = -INFINITY;
-  float z[kJ];
-#pragma unroll
-  for (int j = 0; j < kJ; ++j) z[j] = lane + 64 * j < a.E ? logit_at(a, t, lane + 64 * j) : -INFINITY;
-  if (a.logits != nullptr) {
-#pragma unroll
-    for (int j = 0; j < kJ; ++j)
-      if (lane + 64 * j < a.E) a.logits[static_cast<size_t>(t) * (a.E + 1) + lane + 64 * j] = z[j];
-  }
-  if (lane == 0 && (a.gamma != nullptr || a.logits != nullptr)) {
-    const float zg = logit_at(a, t, a.E);
-    if (a.logits != nullptr) a.logits[static_cast<size_t>(t) * (a.E + 1) + a.E] = zg;
-    if (a.gamma != nullptr) a.gamma[t] = 1.0f / (1.0f + expf(-zg));
-  }
-  float m = -INFINITY;
-  double total = 1.0;
-  if (a.score == MOE_SCORE_SOFTMAX) {
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) m = fmaxf(m, z[j]);
-    m = wave_max(m);
-    double s = 0.0;
-#pragma unroll
-    for (int j = 0; j < kJ; ++j) s += is_off(z[j]) ? 0.0 : soft_ex(z[j], m);
-    total = wave_sum_f64(s);
-  }
-  auto score = [&](float zz) {
-    return a.score == MOE_SCORE_SIGMOID ? 1.0 / (1.0 + exp(-static_cast<double>(zz))) : soft_ex(zz, m) / total;
-  };
+  const bool grouped = a.top_groups < a.n_group;
   uint64_t key[kJ];
 #pragma unroll
   for (int j = 0; j < kJ; ++j) {
     const int e = lane + 64 * j;
     double k = ninf;
-    if (e < a.E && !is_off(z[j])) k = score(z[j]) + (a.bias != nullptr ? static_cast<double>(a.bias[e]) : 0.0);
+    if (e < a.E && !is_off(z[j])) k = score64(a, z[j], sm) + (a.bias != nullptr ? static_cast<double>(a.bias[e]) : 0.0);
     if (!(k > ninf)) k = ninf;
-    if (e < a.E && a.top_groups < a.n_group) keys[e] = k;
+    if (e < a.E && grouped) keys[e] = k;
     key[j] = k > ninf ? order_key64(k) : 0;
   }
-  if (a.top_groups < a.n_group) {
-    // lanes g * L .. g * L + L - 1 scan group g for its two largest keys
-    const int per = a.E / a.n_group;
-    int L = 64;
-    while (L > 1 && 64 / L < a.n_group) L >>= 1;
-    const int g = lane / L;
+  if (grouped) {
     __builtin_amdgcn_wave_barrier();
     __threadfence_block();
-    double b1 = ninf, b2 = ninf;
-    if (g < a.n_group) {
-      for (int i = lane % L; i < per; i += L) {
-        const double k = keys[g * per + i];
-        b2 = fmax(b2, fmin(b1, k));
-        b1 = fmax(b1, k);
-      }
-    }
-    for (int s = 1; s < L; s <<= 1) {
-      const double o1 = shfl_xor_f64(b1, s), o2 = shfl_xor_f64(b2, s);
-      b2 = fmax(fmin(b1, o1), fmax(b2, o2));
-      b1 = fmax(b1, o1);
-    }
-    double rank = b1;
-    if (a.group_top == 2 && b2 > ninf) rank += b2;
-    uint64_t kept = 0;
-    for (int c = 0; c < a.n_group; ++c) {   // group c is kept when fewer than top_groups are before it
-      const double rc = __shfl(rank, c * L, kWave);
-      const bool before = lane % L == 0 && g < a.n_group && (rank > rc || (rank == rc && g < c));
-      if (__popcll(__ballot(before)) < a.top_groups) kept |= 1ull << c;
-    }
-    const float inv = 1.0f / static_cast<float>(per);
+    const uint64_t kept = kept_groups(a, group_rank(a, keys, lane, L), lane, L);
+    const float inv = 1.0f / static_cast<float>(a.E / a.n_group);
 #pragma unroll
     for (int j = 0; j < kJ; ++j) {
       const int e = lane + 64 * j;
-      const int ge = static_cast<int>((static_cast<float>(e) + 0.5f) * inv);   // e / per, exact for e < 1024
-      if (e < a.E && !((kept >> ge) & 1ull)) key[j] = 0;
+      if (e < a.E && !((kept >> group_of(e, inv)) & 1ull)) key[j] = 0;
     }
   }
   int my_e = -1;
@@ -142,7 +167,157 @@ __device__ void select_token(const SelectArgs& a, int t, int lane, double* keys)
       if (e == 64 * j + lane) key[j] = 0;
     if (lane == k) my_e = e;
   }
-  double sc = my_e >= 0 ? score(logit_at(a, t, my_e)) : 0.0;
+  return my_e;
+}
+
+// Candidates from fp32 keys: lane c < n has the expert of fp32 rank c, and the
+// fp64 choice lies among them.  ordered: the first K are its ranks.
+struct Candidates {
+  int e, n;
+  bool open;      // not even that is sure
+  bool ordered;
+};
+// Error of an fp32 key.  exp is the hardware's exp2 (1 ulp) of a product with
+// log2 e: z - m (half an ulp), the constant and the product are off by 2.4 x
+// 2^-24 of up to 150 (beyond, the score is 0 in fp32 and below 2^-149 in fp64),
+// which is a relative error under 2^-15.9 of the exponential; the sum, the
+// hardware's reciprocal (1 ulp) and the softmax's sum (16 + 6 additions) add
+// 2^-19.  So a score above fp32's subnormals is within 2^-15.7 of itself; a
+// sigmoid is within 2^-21.5 and a softmax within 2^-18 of its largest (the
+// product's error times |d| e^-|d| < 0.4); adding the bias rounds by 2^-24 of
+// the key.  Two keys are in order for sure when they differ by more than twice
+// that; two ranks of up to two keys, when by more than four times that at the
+// largest key's magnitude.
+struct Margin {   // two keys of magnitude up to v are in order when they differ by more than rel v + cap
+  float rel, cap;
+};
+__device__ __forceinline__ Margin margin(const SelectArgs& a, float largest_score) {
+  if (a.bias == nullptr) return {0x1p-14f, 0x1p-120f};
+  return {0x1p-22f, a.score == MOE_SCORE_SIGMOID ? 0x1p-20f : 0x1p-17f * largest_score};
+}
+template <int kJ>
+__device__ __forceinline__ Candidates choose32(const SelectArgs& a, const float (&z)[kJ], float m, int lane, int L,
+                                               float* keys) {
+  const float ninf = -INFINITY;
+  const bool grouped = a.top_groups < a.n_group, sigmoid = a.score == MOE_SCORE_SIGMOID;
+  constexpr float kLog2e = 1.44269504f;
+  float s[kJ], total = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
+    s[j] = sigmoid ? __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z[j]))
+                   : (z[j] == m ? 1.0f : __builtin_amdgcn_exp2f(kLog2e * (z[j] - m)));
+    total += is_off(z[j]) ? 0.0f : s[j];
+  }
+  const float inv_total = sigmoid ? 1.0f : __builtin_amdgcn_rcpf(wave_sum(total));
+  uint32_t hi[kJ], lo[kJ];
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
+    const int e = lane + 64 * j;
+    float k = ninf;
+    if (e < a.E && !is_off(z[j])) k = s[j] * inv_total + (a.bias != nullptr ? a.bias[e] : 0.0f);
+    if (!(k > ninf)) k = ninf;
+    if (e < a.E && grouped) keys[e] = k;
+    hi[j] = k > ninf ? order_key(k) : 0u;
+    lo[j] = kJ - 1 - j;
+  }
+  const Margin mg = margin(a, inv_total);
+  Candidates r = {-1, 0, false, true};
+  if (grouped) {
+    __builtin_amdgcn_wave_barrier();
+    __threadfence_block();
+    float big = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) big = hi[j] != 0u ? fmaxf(big, fabsf(key_value(hi[j]))) : big;
+    big = wave_max(big);
+    const float rank = group_rank(a, keys, lane, L);
+    const uint64_t kept = kept_groups(a, rank, lane, L);
+    const bool head = lane % L == 0 && lane / L < a.n_group, in = (kept >> (lane / L)) & 1ull;
+    const float least = -wave_max(head && in ? -rank : ninf), next = wave_max(head && !in ? rank : ninf);
+    // groups without a live expert (-inf) cannot matter, on either side; sums
+    // of two keys near fp32's end might overflow
+    r.open = next > ninf && !(least - next > 2.0f * fmaf(mg.rel, big, mg.cap));
+    r.open = r.open || !(big < 1e38f);
+    const float inv = 1.0f / static_cast<float>(a.E / a.n_group);
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      const int e = lane + 64 * j;
+      if (e < a.E && !((kept >> group_of(e, inv)) & 1ull)) hi[j] = 0u;
+    }
+  }
+  oddeven_merge_sort<kJ>([&](int x, int y) {
+    const bool swap = hi[y] > hi[x] || (hi[y] == hi[x] && lo[y] > lo[x]);
+    const uint32_t hx = hi[x], lx = lo[x];
+    hi[x] = swap ? hi[y] : hx;
+    lo[x] = swap ? lo[y] : lx;
+    hi[y] = swap ? hx : hi[y];
+    lo[y] = swap ? lx : lo[y];
+  });
+  TopkList<kJ> list;
+  list.lo = list.lo_hi8 = 0;
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
+    list.hi[j] = hi[j];
+    if (j < 8) list.lo |= lo[j] << (4 * j);
+    else list.lo_hi8 |= lo[j] << (4 * (j - 8));
+  }
+  list.head = (kJ - 1 - static_cast<int>(list.lo & 0xFu)) * 64 + lane;
+  float prev = 0.0f;
+  bool closed = false;
+  for (int k = 0; k < kWave && !closed; ++k) {
+    uint32_t key;
+    const int e = topk_round(list, lane, key);
+    const float v = key_value(key);
+    // false for inf - inf and next to an infinite key
+    const bool apart = k == 0 || prev - v > fmaf(mg.rel, fmaxf(fabsf(prev), fabsf(v)), mg.cap);
+    closed = key == 0u || (k >= a.K && apart);   // no live expert is left, or a gap behind rank K
+    if (!closed) {
+      r.ordered = r.ordered && apart;
+      r.n = k + 1;
+      r.e = lane == k ? e : r.e;
+      prev = v;
+    }
+  }
+  r.open = r.open || !(closed || wave_max_u32_s(list.hi[0]) == 0u);
+  return r;
+}
+
+// The candidates in the order of their fp64 keys (ties: the lower expert).
+__device__ __forceinline__ int reorder64(const SelectArgs& a, int t, const Candidates& c, const Softmax& sm, int lane,
+                                         double* scratch) {
+  double k = 0.0;
+  if (lane < c.n) k = score64(a, logit_at(a, t, c.e), sm) + (a.bias != nullptr ? static_cast<double>(a.bias[c.e]) : 0.0);
+  int* to = reinterpret_cast<int*>(scratch);
+  int rank = 0;
+  for (int i = 0; i < c.n; ++i) {
+    const double ki = __shfl(k, i, kWave);
+    const int ei = __shfl(c.e, i, kWave);
+    rank += (ki > k || (ki == k && ei < c.e)) ? 1 : 0;
+  }
+  if (lane < c.n) to[rank] = c.e;
+  __builtin_amdgcn_wave_barrier();
+  __threadfence_block();
+  return lane < c.n ? to[lane] : -1;
+}
+
+template <int kJ>
+__device__ __forceinline__ void load_token(const SelectArgs& a, int t, int lane, float (&z)[kJ]) {
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) z[j] = lane + 64 * j < a.E ? logit_at(a, t, lane + 64 * j) : -INFINITY;
+}
+template <int kJ>
+__device__ __forceinline__ float logit_max(const float (&z)[kJ]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) m = fmaxf(m, z[j]);
+  return wave_max(m);
+}
+__device__ __forceinline__ int lanes_per_group(const SelectArgs& a) {   // a power of two: every group has its own
+  int L = 64;
+  while (L > 1 && 64 / L < a.n_group) L >>= 1;
+  return L;
+}
+__device__ __forceinline__ void write_choice(const SelectArgs& a, int t, int lane, int my_e, const Softmax& sm) {
+  double sc = my_e >= 0 ? score64(a, logit_at(a, t, my_e), sm) : 0.0;
   if (a.renorm) {
     const double s = wave_sum_f64(sc);
     sc = s > 0.0 ? sc / s : 0.0;
@@ -151,6 +326,32 @@ __device__ void select_token(const SelectArgs& a, int t, int lane, double* keys)
     a.idx[static_cast<size_t>(t) * a.K + lane] = my_e;
     a.w[static_cast<size_t>(t) * a.K + lane] = static_cast<float>(sc * static_cast<double>(a.scale));
   }
+}
+template <int kJ>
+__device__ __forceinline__ void select_token(const SelectArgs& a, int t, int lane, double* keys) {
+  float z[kJ];
+  load_token<kJ>(a, t, lane, z);
+  if (a.logits != nullptr) {
+#pragma unroll
+    for (int j = 0; j < kJ; ++j)
+      if (lane + 64 * j < a.E) a.logits[static_cast<size_t>(t) * (a.E + 1) + lane + 64 * j] = z[j];
+  }
+  if (lane == 0 && (a.gamma != nullptr || a.logits != nullptr)) {
+    const float zg = logit_at(a, t, a.E);
+    if (a.logits != nullptr) a.logits[static_cast<size_t>(t) * (a.E + 1) + a.E] = zg;
+    if (a.gamma != nullptr) a.gamma[t] = 1.0f / (1.0f + expf(-zg));
+  }
+  Softmax sm = {-INFINITY, 1.0};
+  if (a.score == MOE_SCORE_SOFTMAX) sm.m = logit_max(z);
+  const int L = lanes_per_group(a);
+  const Candidates c = choose32<kJ>(a, z, sm.m, lane, L, reinterpret_cast<float*>(keys));
+  // weights that are renormalised do not need the softmax's sum
+  if (a.score == MOE_SCORE_SOFTMAX && (c.open || !c.ordered || !a.renorm)) sm.total = total64(z, sm.m);
+  int my_e = c.e;
+  if (c.open) my_e = choose64<kJ>(a, z, sm, lane, L, keys);
+  else if (!c.ordered) my_e = reorder64(a, t, c, sm, lane, keys);
+  my_e = lane < a.K ? my_e : -1;
+  write_choice(a, t, lane, my_e, sm);
 }
 
 template <int kJ>

@@ -37,6 +37,12 @@ def check(z, k, kind, bias=None, **kw):
     bad = np.argwhere((idx != ref_i).any(-1)).ravel()
     assert bad.size == 0, f"tokens {bad[:4].tolist()}: {idx[bad[:1]].tolist()} != {ref_i[bad[:1]].tolist()}"
     assert (np.abs(w - ref_w) <= W_TOL * np.abs(ref_w) + 1e-37).all()
+    # the same rows many times over: long batches run on a kernel of their own
+    reps = -(-2051 // len(z))
+    many_i, many_w, _ = run(np.tile(z, (reps, 1)), k, kind, bias, **kw)
+    assert np.array_equal(many_i, np.tile(ref_i, (reps, 1)))
+    ref_many = np.tile(ref_w, (reps, 1))
+    assert (np.abs(many_w - ref_many) <= W_TOL * np.abs(ref_many) + 1e-37).all()
     return idx, w
 
 
@@ -44,6 +50,10 @@ CASES = [  # E, K, T, kind, groups, top_groups, group_top, bias, renorm, scale
     (1, 1, 3, "softmax", 1, 1, 1, False, True, 1.0),
     (2, 2, 5, "sigmoid", 2, 1, 2, True, False, 16.0),
     (64, 64, 9, "sigmoid", 1, 1, 1, True, True, 1.0),
+    (60, 5, 40, "sigmoid", 15, 4, 2, True, True, 1.0),
+    (128, 16, 60, "softmax", 16, 6, 1, True, False, 1.0),
+    (250, 16, 33, "sigmoid", 1, 1, 1, True, False, 2.5),
+    (65, 1, 70, "softmax", 13, 2, 2, False, True, 1.0),
     (65, 7, 70, "softmax", 1, 1, 1, True, False, 2.5),
     (64, 3, 33, "softmax", 64, 5, 2, False, True, 1.0),
     (160, 6, 50, "softmax", 8, 3, 1, False, False, 16.0),
@@ -105,6 +115,26 @@ def test_keys_nearer_than_a_rounding(kind, groups):
 
 
 @pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_group_ranks_of_cancelling_keys(kind):
+    # the two best keys of every group nearly cancel, so ranks differ by less
+    # than the keys' own rounding; and far-down logits whose scores leave fp32
+    rng = np.random.default_rng(6)
+    T, G, per = 50, 16, 8
+    z = rng.standard_normal((T, G * per)).astype(np.float32)
+    bias = np.full((G, per), -3e4, np.float32)
+    bias[:, 2] = 1000.0 + np.arange(G) % 3
+    bias[:, 5] = -bias[:, 2]
+    check(z, 5, kind, bias.ravel(), n_group=G, top_groups=3, group_top=2)
+    bias[:, 2], bias[:, 5] = 3e38, -3e38
+    check(z, 5, kind, bias.ravel(), n_group=G, top_groups=3, group_top=2)
+    bias[:, [2, 5]] = -3.3e38
+    check(z, 5, kind, bias.ravel(), n_group=G, top_groups=3, group_top=2)
+    check(-95 + 8 * z, 20, kind)
+    z[:, 0] = 30.0
+    check(-70 + 10 * z, 20, kind, n_group=G, top_groups=3, group_top=2)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
 def test_extreme_values(kind):
     big = float(np.finfo(np.float32).max)
     rows = [[-big] * 8, [-big, 0, -big, 1, -big, -big, 2, -big], [big, -big, big, 0, 1, 2, 3, 4],
@@ -118,9 +148,10 @@ def test_extreme_values(kind):
             check(rows, 2, kind, bias, n_group=4, top_groups=2, group_top=gt)
 
 
-def test_shared_gate_column_and_stride():
+@pytest.mark.parametrize("T", [37, 3001])
+def test_shared_gate_column_and_stride(T):
     rng = np.random.default_rng(9)
-    z = rng.standard_normal((37, 101)).astype(np.float32)
+    z = rng.standard_normal((T, 101)).astype(np.float32)
     idx, w, g = run(z, 5, "sigmoid", gate=True)
     ref_i, ref_w = so.select(z[:, :100], 5, "sigmoid")
     assert np.array_equal(idx, ref_i)
