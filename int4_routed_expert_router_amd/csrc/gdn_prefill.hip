@@ -199,12 +199,30 @@ __device__ __forceinline__ float col_max(float v) {
 __device__ __forceinline__ float col_sum(float v) {
   return col_reduce(v, [](float a, float b) { return a + b; });
 }
+// Inclusive prefix sum over the wave: row shifts within 16 lanes, then the
+// totals of the rows before.
+template <int kCtrl>
+__device__ __forceinline__ double dpp_f64_or0(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = dpp_upd_u32<kCtrl, 0xF>(static_cast<uint32_t>(u), 0u);
+  const uint32_t hi = dpp_upd_u32<kCtrl, 0xF>(static_cast<uint32_t>(u >> 32), 0u);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), lane);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), lane);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
 __device__ __forceinline__ double scan_f64(double v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double o = __shfl_up(v, d, kWave);
-    if (lane >= d) v += o;
-  }
+  v += dpp_f64_or0<0x111>(v);   // row_shr 1, 2, 4, 8 (0 where no lane is that far back)
+  v += dpp_f64_or0<0x112>(v);
+  v += dpp_f64_or0<0x114>(v);
+  v += dpp_f64_or0<0x118>(v);
+  const double r0 = lane_f64(v, 15), r1 = lane_f64(v, 31), r2 = lane_f64(v, 47);
+  if (lane >= 16) v += r0;
+  if (lane >= 32) v += r1;
+  if (lane >= 48) v += r2;
   return v;
 }
 
@@ -230,6 +248,10 @@ __device__ __forceinline__ bool find_block(const GdnArgs& a, int slot, int lane,
   return len > 0 && end - begin > kShort;
 }
 
+// 2^x by the hardware's exp2 of x rounded to fp32: off by |x| 2^-24 of the
+// result, which is |x| 2^x 2^-24 < 2^-24 of 1
+__device__ __forceinline__ float exp2_of(double x) { return __builtin_amdgcn_exp2f(static_cast<float>(x)); }
+
 // 16x16x16 product in fp32: acc += X Y with X rows from LDS (x: lane's row,
 // columns 4q .. 4q+3) and Y as a result tile (lane: column lane%16, rows 4q+r)
 __device__ __forceinline__ f32x4 mul16(float4 x, f32x4 y, f32x4 acc) {
@@ -250,6 +272,7 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
   __shared__ double Gs[kBlock];
   __shared__ float bs[kBlock], rks[kBlock], rqs[kBlock];
   __shared__ float wmax[4][2];
+  __shared__ bool grows;   // some decay is above 1
   float* As = reinterpret_cast<float*>(ks);   // takes the place of the keys once their products are done
   float* Ps = reinterpret_cast<float*>(qs);
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, q = lane >> 4;
@@ -299,49 +322,21 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
   float* vec = reinterpret_cast<float*>(ws + prefill_ws_heads(a) + (static_cast<size_t>(slot) * a.Hv + h) * kHeadBytes +
                                         24 * 1024);
   if (w == 0) {
-    // log decays are summed in fp64: differences of sums far from 0 keep their
-    // digits (a block of strong decays reaches -1000 and below).  -inf counts
-    // as -1000, which clears the state just as well (e^-1000 = 0 in fp32).
+    // log decays are summed in fp64, in units of log 2: differences of sums far
+    // from 0 keep their digits (a block of strong decays reaches -1000 and
+    // below).  -inf counts as -1000, which clears the state just as well
+    // (e^-1000 = 0 in fp32).
     const size_t at = static_cast<size_t>(tok0 + min(lane, len - 1)) * a.Hv + h;
     const bool ok = lane < len;
     float gt = ok ? a.g[at] : 0.0f;
     gt = gt < -1000.0f ? -1000.0f : gt;
-    const float bt = ok ? a.beta[at] : 0.0f;
-    const double G = scan_f64(static_cast<double>(gt), lane);
-    Gs[lane] = G;
-    bs[lane] = bt;
-    const double last = __shfl(G, 63, kWave);
-    const float eg = expf(static_cast<float>(G)), left = expf(static_cast<float>(last - G));
-    // bounds on what the block makes of a state row of norm s and values up to
-    // v (per state row), for the scales of the pairs: |R| <= v + gmax s,
-    // |e^(G_last - G) rk D| <= d0 v + d1 s, |S'| <= s0 v + s1 s.  The factors
-    // I - beta k k^T have norm max(1, |1 - beta|), rk <= 2^-12 (rows are scaled
-    // to a largest value of 2^12 or more).  With beta in [0, 2] and g <= 0,
-    // rho = rmax = 1 and gmax <= 1.
-    const float gmax = wave_max(eg), bmax = wave_max(fabsf(bt));
-    float rho = fmaxf(1.0f, fabsf(1.0f - bt));
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) rho *= __shfl_xor(rho, d, kWave);
-    const float up = wave_max(static_cast<float>(G)), dn = -wave_max(-static_cast<float>(G));
-    const float rmax = __ballot(gt > 0.0f) ? expf(fmaxf(up, 0.0f) - fminf(dn, 0.0f)) : 1.0f;
-    const float sb = wave_sum(fabsf(bt)) * rmax, sg = wave_sum(fabsf(bt) * left);
-    const float dd = bmax * rmax * 0x1p-12f;
-    if (lane == 0) {
-      vec[kScGamma] = expf(static_cast<float>(last));
-      vec[kScGmax] = gmax;
-      vec[kScD0] = dd * (1.0f + rho * sb);
-      vec[kScD1] = dd * rho * gmax;
-      vec[kScS0] = rho * sg;
-      vec[kScS1] = rho * expf(static_cast<float>(last));
-    }
+    Gs[lane] = scan_f64(static_cast<double>(gt) * 1.4426950408889634, lane);
+    bs[lane] = ok ? a.beta[at] : 0.0f;
+    // not from the sums, which may rise by a rounding where g is 0
+    const bool any = __ballot(gt > 0.0f) != 0ull;
+    if (lane == 0) grows = any;
   }
   __syncthreads();
-  if (w == 0) {
-    const float eg = expf(static_cast<float>(Gs[lane]));
-    vec[lane] = eg * rks[lane];
-    vec[64 + lane] = eg;
-    vec[128 + lane] = rqs[lane];
-  }
   if (h % rep == 0) {   // the key head's operands, once
     uint4* out = reinterpret_cast<uint4*>(ws + (static_cast<size_t>(slot) * a.Hk + hk) * kKeyBytes);
 #pragma unroll
@@ -381,6 +376,7 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
     }
   }
   __syncthreads();
+  f32x4 diag = {0, 0, 0, 0};   // A's diagonal block w
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (j <= w) {
@@ -390,32 +386,65 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * w + 4 * q + r;
-        const float e = expf(static_cast<float>(Gs[t] - Gc)) * rc;
-        As[t * kRowF + c] = c < t ? bs[t] * rks[t] * e * kk[j][r] : 0.0f;
+        const float e = exp2_of(Gs[t] - Gc) * rc;
+        const float av = c < t ? bs[t] * rks[t] * e * kk[j][r] : 0.0f;
+        if (j < w) As[t * kRowF + c] = av;
+        else diag[r] = av;
         Ps[t * kRowF + c] = c <= t ? e * qk[j][r] : 0.0f;
       }
     }
   }
-  __syncthreads();
-  // column n of the inverse of diagonal block w (the four lane groups alike)
+  // column n of the inverse of I + diagonal block w (the four lane groups
+  // alike): x_i = [i = n] - sum_j A_ij x_j, A_ij taken from the lane that has it
   f32x4 tcol[4];
   {
     float x[16];
-    const float* blk = As + 16 * w * kRowF + 16 * w;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float v = i == n ? 1.0f : 0.0f;
 #pragma unroll
-      for (int j = 0; j < i; ++j) v = fmaf(-blk[i * kRowF + j], x[j], v);
+      for (int j = 0; j < i; ++j) {
+        const float aij = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(
+            static_cast<int>(__float_as_uint(diag[i & 3])), 16 * (i >> 2) + j)));
+        v = fmaf(-aij, x[j], v);
+      }
       x[i] = v;
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) tcol[0][r] = q == 0 ? x[r] : q == 1 ? x[4 + r] : q == 2 ? x[8 + r] : x[12 + r];
   }
-  __syncthreads();   // the block is read by its own wave alone, but let every wave finish first
 #pragma unroll
   for (int r = 0; r < 4; ++r) As[(16 * w + 4 * q + r) * kRowF + 16 * w + n] = tcol[0][r];
   __syncthreads();
+  if (w == 3) {   // the wave with the fewest blocks of T and M: the block's vectors and scalars
+    const double G = Gs[lane], last = Gs[63];
+    const float bt = bs[lane], eg = exp2_of(G), left = exp2_of(last - G);
+    vec[lane] = eg * rks[lane];
+    vec[64 + lane] = eg;
+    vec[128 + lane] = rqs[lane];
+    // bounds on what the block makes of a state row of norm s and values up to
+    // v (per state row), for the scales of the pairs: |R| <= v + gmax s,
+    // |e^(G_last - G) rk D| <= d0 v + d1 s, |S'| <= s0 v + s1 s.  The factors
+    // I - beta k k^T have norm max(1, |1 - beta|), rk <= 2^-12 (rows are scaled
+    // to a largest value of 2^12 or more).  With beta in [0, 2] and g <= 0,
+    // rho = rmax = 1 and gmax <= 1.
+    const float gmax = wave_max(eg), bmax = wave_max(fabsf(bt));
+    const float rho = __uint_as_float(wave_allreduce_u32(
+        __float_as_uint(fmaxf(1.0f, fabsf(1.0f - bt))),
+        [](uint32_t x, uint32_t y) { return __float_as_uint(__uint_as_float(x) * __uint_as_float(y)); }));
+    const float up = wave_max(static_cast<float>(G)), dn = -wave_max(-static_cast<float>(G));
+    const float rmax = grows ? __builtin_amdgcn_exp2f(fmaxf(up, 0.0f) - fminf(dn, 0.0f)) : 1.0f;
+    const float sb = wave_sum(fabsf(bt)) * rmax, sg = wave_sum(fabsf(bt) * left);
+    const float dd = bmax * rmax * 0x1p-12f, gamma = exp2_of(last);
+    if (lane == 0) {
+      vec[kScGamma] = gamma;
+      vec[kScGmax] = gmax;
+      vec[kScD0] = dd * (1.0f + rho * sb);
+      vec[kScD1] = dd * rho * gmax;
+      vec[kScS0] = rho * sg;
+      vec[kScS1] = rho * gamma;
+    }
+  }
   auto rows = [&](const float* m, int i, int k) {   // operand rows of block (i, k)
     return *reinterpret_cast<const float4*>(m + (16 * i + n) * kRowF + 16 * k + 4 * q);
   };
@@ -448,7 +477,7 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * (w + d) + 4 * q + r;
-        tcol[d][r] *= bc * (expf(static_cast<float>(last - Gs[t])) * rks[t]);
+        tcol[d][r] *= bc * (exp2_of(last - Gs[t]) * rks[t]);
         mcol[d][r] *= bc;
         // a non-finite query row must not set the scale of the others
         const float at = fabsf(tcol[d][r]), am = fabsf(mcol[d][r]);
