@@ -270,7 +270,7 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
   __shared__ __attribute__((aligned(16))) uint16_t ks[kBlock * kRow];
   __shared__ __attribute__((aligned(16))) uint16_t qs[kBlock * kRow];
   __shared__ double Gs[kBlock];
-  __shared__ float bs[kBlock], rks[kBlock], rqs[kBlock];
+  __shared__ float bs[kBlock], rks[kBlock], rqs[kBlock], lr[kBlock];   // lr: e^(G_last - G) rk
   __shared__ float wmax[4][2];
   __shared__ bool grows;   // some decay is above 1
   float* As = reinterpret_cast<float*>(ks);   // takes the place of the keys once their products are done
@@ -337,6 +337,7 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
     if (lane == 0) grows = any;
   }
   __syncthreads();
+  if (w == 0) lr[lane] = exp2_of(Gs[63] - Gs[lane]) * rks[lane];   // read after the next barrier
   if (h % rep == 0) {   // the key head's operands, once
     uint4* out = reinterpret_cast<uint4*>(ws + (static_cast<size_t>(slot) * a.Hk + hk) * kKeyBytes);
 #pragma unroll
@@ -376,18 +377,28 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
     }
   }
   __syncthreads();
+  // the lane's rows and columns, read before the products are stored (the
+  // compiler would read them again after every store)
+  double Gt[4], Gc[4];
+  float bt[4], rc[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int t = 16 * w + 4 * q + r;
+    Gt[r] = Gs[t];
+    bt[r] = bs[t] * rks[t];
+    Gc[r] = Gs[16 * r + n];
+    rc[r] = rks[16 * r + n];
+  }
   f32x4 diag = {0, 0, 0, 0};   // A's diagonal block w
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (j <= w) {
       const int c = 16 * j + n;
-      const double Gc = Gs[c];
-      const float rc = rks[c];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * w + 4 * q + r;
-        const float e = exp2_of(Gs[t] - Gc) * rc;
-        const float av = c < t ? bs[t] * rks[t] * e * kk[j][r] : 0.0f;
+        const float e = exp2_of(Gt[r] - Gc[j]) * rc[j];
+        const float av = c < t ? bt[r] * e * kk[j][r] : 0.0f;
         if (j < w) As[t * kRowF + c] = av;
         else diag[r] = av;
         Ps[t * kRowF + c] = c <= t ? e * qk[j][r] : 0.0f;
@@ -395,20 +406,22 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
     }
   }
   // column n of the inverse of I + diagonal block w (the four lane groups
-  // alike): x_i = [i = n] - sum_j A_ij x_j, A_ij taken from the lane that has it
+  // alike): x starts as column n of I; then for j = 0, 1, ...: x_i -= A_ij x_j
+  // for all i > j at once, A_ij taken from the lane that has it
   f32x4 tcol[4];
   {
     float x[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = i == n ? 1.0f : 0.0f;
+    for (int i = 0; i < 16; ++i) x[i] = i == n ? 1.0f : 0.0f;
 #pragma unroll
-      for (int j = 0; j < i; ++j) {
+    for (int j = 0; j < 15; ++j) {
+#pragma unroll
+      for (int i = j + 1; i < 16; ++i) {
         const float aij = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(
             static_cast<int>(__float_as_uint(diag[i & 3])), 16 * (i >> 2) + j)));
-        v = fmaf(-aij, x[j], v);
+        x[i] = fmaf(-aij, x[j], x[i]);
       }
-      x[i] = v;
+      __builtin_amdgcn_sched_barrier(0);   // keeps the column's 15 scalars at most alive
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) tcol[0][r] = q == 0 ? x[r] : q == 1 ? x[4 + r] : q == 2 ? x[8 + r] : x[12 + r];
@@ -470,14 +483,13 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
     }
   }
   const float bc = bs[16 * w + n];
-  const double last = Gs[63];
 #pragma unroll
   for (int d = 0; d < 4; ++d) {
     if (w + d < 4) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = 16 * (w + d) + 4 * q + r;
-        tcol[d][r] *= bc * (exp2_of(last - Gs[t]) * rks[t]);
+        tcol[d][r] *= bc * lr[t];
         mcol[d][r] *= bc;
         // a non-finite query row must not set the scale of the others
         const float at = fabsf(tcol[d][r]), am = fabsf(mcol[d][r]);
