@@ -31,18 +31,20 @@ __device__ __forceinline__ void seq_range(const GdnArgs& a, int b, int& begin, i
 }
 
 // ---- token by token ---------------------------------------------------------
-// A row of 16 lanes owns NS state rows in registers (rows row0 + 16 z), lane
-// l16 their columns 8 l16 .. 8 l16 + 7.  Runs tokens [t0, t1) of one sequence
-// and value head.
+// A row of 16 lanes owns NS state rows in registers (row0 + 16 z, those below
+// d_v), lane l16 their columns 8 l16 .. 8 l16 + 7.  Runs tokens [t0, t1) of
+// one sequence and value head in fp32; the next token's loads are in flight
+// meanwhile.  A row's arithmetic does not depend on NS.
 template <int ACT, int NS>
 __device__ __forceinline__ void run_tokens(const GdnArgs& a, int b, int h, int t0, int t1, int row0) {
   const int hk = h / (a.Hv / a.Hk), c0 = 8 * (threadIdx.x & 15);
   float* srow[NS];
   float s[NS][8];
+  int row[NS];
 #pragma unroll
   for (int z = 0; z < NS; ++z) {
-    const int row = min(row0 + 16 * z, a.dv - 1);
-    srow[z] = a.state + ((static_cast<size_t>(b) * a.Hv + h) * a.dv + row) * kDK + c0;
+    row[z] = NS == 1 ? row0 : min(row0 + 16 * z, a.dv - 1);
+    srow[z] = a.state + ((static_cast<size_t>(b) * a.Hv + h) * a.dv + row[z]) * kDK + c0;
     *reinterpret_cast<float4*>(s[z]) = *reinterpret_cast<const float4*>(srow[z]);
     *reinterpret_cast<float4*>(s[z] + 4) = *reinterpret_cast<const float4*>(srow[z] + 4);
   }
@@ -54,14 +56,16 @@ __device__ __forceinline__ void run_tokens(const GdnArgs& a, int b, int h, int t
     qv = *reinterpret_cast<const uint4*>(a.q + qk);
     kv = *reinterpret_cast<const uint4*>(a.k + qk);
 #pragma unroll
-    for (int z = 0; z < NS; ++z) vv[z] = a.v[hv * a.dv + min(row0 + 16 * z, a.dv - 1)];
+    for (int z = 0; z < NS; ++z) vv[z] = a.v[hv * a.dv + row[z]];
     gv = a.g[hv];
     bv = a.beta[hv];
   };
   load(t0);
   for (int t = t0; t < t1; ++t) {
     const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, kw[4] = {kv.x, kv.y, kv.z, kv.w};
-    const float alpha = expf(gv), bt = bv;
+    // the hardware's exp2 and 1/sqrt, each within an ulp; x log2(e) is off by
+    // |x| 2^-24 of the decay at most
+    const float alpha = __builtin_amdgcn_exp2f(gv * 1.44269504f), bt = bv;
     float vt[NS];
 #pragma unroll
     for (int z = 0; z < NS; ++z) vt[z] = act_to_f32<ACT>(vv[z]);
@@ -78,7 +82,8 @@ __device__ __forceinline__ void run_tokens(const GdnArgs& a, int b, int h, int t
     qq = row_sum16(qq);
     kk = row_sum16(kk);
     kq = row_sum16(kq);
-    const float rq = a.q_scale / sqrtf(qq + kEps), rk = 1.0f / sqrtf(kk + kEps);
+    const float rq = a.q_scale * __builtin_amdgcn_rsqf(qq + kEps), rk = __builtin_amdgcn_rsqf(kk + kEps);
+    float* o = a.o + (static_cast<size_t>(t) * a.Hv + h) * a.dv;
 #pragma unroll
     for (int z = 0; z < NS; ++z) {
       float u = 0, w = 0;
@@ -89,31 +94,42 @@ __device__ __forceinline__ void run_tokens(const GdnArgs& a, int b, int h, int t
       }
       u = row_sum16(u);
       w = row_sum16(w);
-      const float d = bt * (vt[z] - alpha * (u * rk)), dk = d * rk;
+      const float d = bt * fmaf(-alpha, u * rk, vt[z]), dk = d * rk;
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[z][j] = fmaf(dk, kn[j], alpha * s[z][j]);
-      if (c0 == 0 && row0 + 16 * z < a.dv)
-        a.o[(static_cast<size_t>(t) * a.Hv + h) * a.dv + row0 + 16 * z] = fmaf(dk * rq, kq, alpha * (w * rq));
+      if (c0 == 0 && (NS == 1 || row0 + 16 * z < a.dv)) o[row[z]] = fmaf(dk * rq, kq, alpha * (w * rq));
     }
   }
 #pragma unroll
   for (int z = 0; z < NS; ++z) {
-    if (row0 + 16 * z < a.dv) {
+    if (NS == 1 || row0 + 16 * z < a.dv) {
       *reinterpret_cast<float4*>(srow[z]) = *reinterpret_cast<const float4*>(s[z]);
       *reinterpret_cast<float4*>(srow[z] + 4) = *reinterpret_cast<const float4*>(s[z] + 4);
     }
   }
 }
 
-// Every sequence token by token (calls of at most kShort tokens in all): one
-// workgroup per (16 state rows, value head, sequence).
-template <int ACT>
+// Sequences up to this length go token by token, longer ones in blocks (32
+// value heads of 128; token by token against blocks, us): 20 tokens 10.0
+// against 15.9 for one sequence, 33 against 41 for 8, 174 against 219 for 64;
+// 24 tokens 11.3 / 15.9, 38 / 41, 203 / 223; 32 tokens 14.1 / 15.9, 46 / 41,
+// 261 / 230.
+constexpr int kShort = 24;
+
+// The sequences of at most kShort tokens: one workgroup per (16 NS state rows,
+// value head, sequence).  With NS = 1 most of a token's arithmetic is the
+// conversion and the norms of its q and k, the same in every row; 4 rows per
+// lane share it.  64 sequences of 8 tokens with 32 heads of 128: 91 us, 268 MB
+// of state at 2.9 TB/s, bound by the vector arithmetic; 16 tokens of one
+// sequence: 6 us, bound by the latency of a token's chain of sums.
+template <int ACT, int NS>
 __global__ __launch_bounds__(256) void k_gdn_tokens(GdnArgs a) {
-  const int slices = a.dv / 16;
+  const int slices = (a.dv + 16 * NS - 1) / (16 * NS);
   int t0, t1;
   seq_range(a, blockIdx.y, t0, t1);
-  if (t0 < t1)
-    run_tokens<ACT, 1>(a, blockIdx.y, blockIdx.x / slices, t0, t1, (blockIdx.x % slices) * 16 + (threadIdx.x >> 4));
+  if (t0 < t1 && t1 - t0 <= kShort)
+    run_tokens<ACT, NS>(a, blockIdx.y, blockIdx.x / slices, t0, t1,
+                        (blockIdx.x % slices) * 16 * NS + (threadIdx.x >> 4));
 }
 
 // ---- in blocks of 64 tokens -------------------------------------------------
@@ -135,7 +151,6 @@ __global__ __launch_bounds__(256) void k_gdn_tokens(GdnArgs a) {
 // against another pair; fp32 matrix instructions take 8 times as long as
 // fp16's for the same product.
 constexpr int kBlock = 64;         // tokens of a block
-constexpr int kShort = 16;         // sequences up to this length go token by token
 constexpr int kRow = 136;          // LDS row of 128 fp16 values, padded
 constexpr int kRowF = 68;          // the same bytes as fp32 values
 
@@ -557,7 +572,7 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
   }
 }
 
-// One workgroup per (sequence, value head, 16 NS state rows), its sequence's
+// One workgroup per (sequence, value head, 16 state rows), its sequence's
 // blocks in order.  Wave w holds key columns 32w .. 32w+31 of the state rows
 // (result tiles: lane's column = state row) and forms tile row w of R, D and O:
 //   S pair -> LDS | K S^T, R pair -> LDS | T R = D pair -> LDS | S += D^T K.
@@ -567,27 +582,27 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
 // order, so the values, which are needed first, are loaded two blocks ahead.
 // One wave per SIMD is enough work only for long batches; the chain of a
 // single sequence is bound by its latency (LDS exchanges, dependent products).
-template <int ACT, int NS>
+template <int ACT>
 __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* __restrict__ ws) {
-  __shared__ f16x8 sf[NS][4][2][64];
-  __shared__ f16x4 rf[NS][2][2][64][2];
-  __shared__ f16x4 df[NS][2][2][64][2];
-  __shared__ float ssum[NS][4][16];   // per wave and state row: sum of squares of the scaled state
-  __shared__ float vmax[NS][4][16];   // per wave and state row: largest value of the next block
+  __shared__ f16x8 sf[4][2][64];
+  __shared__ f16x4 rf[2][2][64][2];
+  __shared__ f16x4 df[2][2][64][2];
+  __shared__ float ssum[4][16];   // per wave and state row: sum of squares of the scaled state
+  __shared__ float vmax[4][16];   // per wave and state row: largest value of the next block
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   // a sequence's workgroups are dealt to the eight dies in runs, so that the
   // workgroups that read one key head's operands share an L2
-  const int slices = (a.dv + 16 * NS - 1) / (16 * NS), units = a.Hv * slices, run = (units + 7) / 8;
+  const int slices = a.dv / 16, units = a.Hv * slices, run = (units + 7) / 8;
   const int b = blockIdx.x / (8 * run), i = blockIdx.x % (8 * run);
   const int unit = (i % 8) * run + i / 8;
   if (unit >= units) return;
-  const int h = unit / slices, dv0 = (unit % slices) * 16 * NS;
+  const int h = unit / slices, dv0 = (unit % slices) * 16;
   int t0, t1;
   seq_range(a, b, t0, t1);
   if (t0 == t1) return;
-  if (t1 - t0 <= kShort) {
-    run_tokens<ACT, NS>(a, b, h, t0, t1, dv0 + (tid >> 4));
+  if (t1 - t0 <= kShort) {   // in a batch they are k_gdn_tokens'
+    if (a.B == 1) run_tokens<ACT, 1>(a, b, h, t0, t1, dv0 + (tid >> 4));
     return;
   }
   t0 = __builtin_amdgcn_readfirstlane(t0);
@@ -600,25 +615,12 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
   const uint32_t row_el = static_cast<uint32_t>(a.Hv) * a.dv;
   const uint16_t* vbase = a.v + (static_cast<size_t>(t0 + 16 * w) * a.Hv + h) * a.dv;
   float* obase = a.o + (static_cast<size_t>(t0 + 16 * w) * a.Hv + h) * a.dv;
-  uint32_t el[NS];   // element of row 4q, state row of the lane (a valid one for rows past the last)
-  bool row_ok[NS];
-#pragma unroll
-  for (int z = 0; z < NS; ++z) {
-    row_ok[z] = dv0 + 16 * z < a.dv;   // uniform: d_v is a multiple of 16
-    el[z] = 4u * q * row_el + min(dv0 + 16 * z + n, a.dv - 1);
-  }
+  const uint32_t el = 4u * q * row_el + dv0 + n;   // element of row 4q, state row of the lane
 
-  f32x4 S[NS][2];
-  float* sp[NS];
-#pragma unroll
-  for (int z = 0; z < NS; ++z) {
-    const int row = min(dv0 + 16 * z + n, a.dv - 1);
-    sp[z] = a.state + ((static_cast<size_t>(b) * a.Hv + h) * a.dv + row) * kDK + 32 * w + 4 * q;
-    S[z][0] = *reinterpret_cast<const f32x4*>(sp[z]);
-    S[z][1] = *reinterpret_cast<const f32x4*>(sp[z] + 16);
-  }
+  float* sp = a.state + ((static_cast<size_t>(b) * a.Hv + h) * a.dv + dv0 + n) * kDK + 32 * w + 4 * q;
+  f32x4 S[2] = {*reinterpret_cast<const f32x4*>(sp), *reinterpret_cast<const f32x4*>(sp + 16)};
   uint4 kf[4], qf[4], kt[4], th[2], tl[2], mh[2], ml[2];
-  uint16_t va[NS][4], vb[NS][4];   // values of even and odd blocks
+  uint16_t va[4], vb[4];   // values of even and odd blocks
   float4 ev, rv;
   struct Scalars {
     float4 a, b;   // kScGamma .. kScGmax, kScD0 .. kScS1
@@ -670,37 +672,30 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
 #pragma unroll
     for (int f = 0; f < 4; ++f) kt[f] = frag(pk + 32768 + w * 4096, 1024 * f);
   };
-  auto load_values = [&](int c, uint16_t (&vv)[NS][4]) {
+  auto load_values = [&](int c, uint16_t (&vv)[4]) {
     const uint16_t* p = vbase + static_cast<size_t>(c) * kBlock * row_el;
     if (t0 + (c + 1) * kBlock <= t1) {   // uniform
 #pragma unroll
-      for (int z = 0; z < NS; ++z)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) vv[z][r] = *(p + r * row_el + el[z]);
+      for (int r = 0; r < 4; ++r) vv[r] = *(p + r * row_el + el);
     } else {   // rows past the end repeat the sequence's last token (masked at use)
 #pragma unroll
-      for (int z = 0; z < NS; ++z)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int t = min(t0 + c * kBlock + 16 * w + 4 * q + r, t1 - 1);
-          vv[z][r] = a.v[(static_cast<size_t>(t) * a.Hv + h) * a.dv + min(dv0 + 16 * z + n, a.dv - 1)];
-        }
+      for (int r = 0; r < 4; ++r) {
+        const int t = min(t0 + c * kBlock + 16 * w + 4 * q + r, t1 - 1);
+        vv[r] = a.v[(static_cast<size_t>(t) * a.Hv + h) * a.dv + dv0 + n];
+      }
     }
   };
   // masks the block's values and leaves their largest magnitude in LDS
-  auto prepare_values = [&](int c, uint16_t (&vv)[NS][4]) {
+  auto prepare_values = [&](int c, uint16_t (&vv)[4]) {
     const int left = t1 - (t0 + c * kBlock + 16 * w);   // uniform
+    if (left < 16) {
 #pragma unroll
-    for (int z = 0; z < NS; ++z) {
-      float m = 0.0f;
-      if (left < 16) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) vv[z][r] = 4 * q + r < left ? vv[z][r] : 0;
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(act_to_f32<ACT>(vv[z][r])));
-      vmax[z][w][n] = col_max(m);   // the same from the four lanes of a column
+      for (int r = 0; r < 4; ++r) vv[r] = 4 * q + r < left ? vv[r] : 0;
     }
+    float m = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) m = fmaxf(m, fabsf(act_to_f32<ACT>(vv[r])));
+    vmax[w][n] = col_max(m);   // the same from the four lanes of a column
   };
   load_values(0, va);
   load_scalars(hp, sc0);
@@ -711,212 +706,173 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
   load_cols(kp);
   load_values(1, vb);
 
-  // bound[z]: on the norm of the lane's state row (exact at first)
-  float bound[NS];
-#pragma unroll
-  for (int z = 0; z < NS; ++z) {
+  // the largest values of the state rows
+  {
     float m = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) m = fmaxf(m, fmaxf(fabsf(S[z][0][r]), fabsf(S[z][1][r])));
-    ssum[z][w][n] = col_max(m);
+    for (int r = 0; r < 4; ++r) m = fmaxf(m, fmaxf(fabsf(S[0][r]), fabsf(S[1][r])));
+    ssum[w][n] = col_max(m);
   }
   prepare_values(0, va);
   __syncthreads();
-#pragma unroll
-  for (int z = 0; z < NS; ++z)   // 128 elements: norm <= 11.4 times the largest
-    bound[z] = 11.4f * fmaxf(fmaxf(ssum[z][0][n], ssum[z][1][n]), fmaxf(ssum[z][2][n], ssum[z][3][n]));
+  // bound on the norm of the lane's state row; at first from its largest value
+  // (128 elements: at most 11.4 times it), then from exact sums
+  float bound = 11.4f * fmaxf(fmaxf(ssum[0][n], ssum[1][n]), fmaxf(ssum[2][n], ssum[3][n]));
   __syncthreads();
 
-  auto block = [&](int c, uint16_t (&vv)[NS][4], uint16_t (&vnext)[NS][4], const Scalars& sc, Scalars& scnext) {
+  auto block = [&](int c, uint16_t (&vv)[4], uint16_t (&vnext)[4], const Scalars& sc, Scalars& scnext) {
     const bool more = c + 1 < nblk;
     const uint8_t* kn = more ? kp + kstep : kp;
     const uint8_t* hn = more ? hp + hstep : hp;
     load_scalars(hn, scnext);
     const float gamma = sc.a.x, inv_t = sc.a.y, inv_m = sc.a.z, gmax = sc.a.w, cd0 = sc.b.x, cd1 = sc.b.y,
                 cs0 = sc.b.z, cs1 = sc.b.w;
-    float inv_s[NS], fd[NS], fo[NS], inv_d[NS], vs[NS][4], as[NS][4];
+    float inv_s, fd, fo, inv_d, vs[4], as[4];
     // S pair
-#pragma unroll
-    for (int z = 0; z < NS; ++z) {
-      const Pow2 p = pow2_scale(bound[z]);
-      inv_s[z] = p.down;
+    {
+      const Pow2 p = pow2_scale(bound);
+      inv_s = p.down;
       f16x8 hi, lo;
       float ss = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float x = S[z][j >> 2][j & 3] * p.up;   // scaled: its square cannot overflow
+        const float x = S[j >> 2][j & 3] * p.up;   // scaled: its square cannot overflow
         _Float16 vh, vl;
         split16(x, vh, vl);
         hi[j] = vh;
         lo[j] = vl;
         ss = fmaf(x, x, ss);
       }
-      sf[z][w][0][lane] = hi;
-      sf[z][w][1][lane] = lo;
-      ssum[z][w][n] = col_sum(ss);
+      sf[w][0][lane] = hi;
+      sf[w][1][lane] = lo;
+      ssum[w][n] = col_sum(ss);
     }
     // scales of R and D from the bounds; V and e^G rk under R's scale
-#pragma unroll
-    for (int z = 0; z < NS; ++z) {
-      const float vm = fmaxf(fmaxf(vmax[z][0][n], vmax[z][1][n]), fmaxf(vmax[z][2][n], vmax[z][3][n]));
-      const Pow2 pr = pow2_scale(fmaf(gmax, bound[z], vm)), pd = pow2_scale(fmaf(cd1, bound[z], cd0 * vm));
-      fd[z] = inv_t * pr.down * pd.up;
-      fo[z] = inv_m * pr.down;
-      inv_d[z] = pd.down;
-      bound[z] = cs0 * vm;   // the next block's, completed below
+    {
+      const float vm = fmaxf(fmaxf(vmax[0][n], vmax[1][n]), fmaxf(vmax[2][n], vmax[3][n]));
+      const Pow2 pr = pow2_scale(fmaf(gmax, bound, vm)), pd = pow2_scale(fmaf(cd1, bound, cd0 * vm));
+      fd = inv_t * pr.down * pd.up;
+      fo = inv_m * pr.down;
+      inv_d = pd.down;
+      bound = cs0 * vm;   // the next block's, completed below
       const float at[4] = {sc.eg.x, sc.eg.y, sc.eg.z, sc.eg.w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        vs[z][r] = act_to_f32<ACT>(vv[z][r]) * pr.up;
-        as[z][r] = at[r] * (inv_s[z] * pr.up);
+        vs[r] = act_to_f32<ACT>(vv[r]) * pr.up;
+        as[r] = at[r] * (inv_s * pr.up);
       }
     }
     __syncthreads();
     // K S^T and the R pair
-    f16x8 sh[NS][4], sl[NS][4];
-    f32x4 X[NS][2];
-#pragma unroll
-    for (int z = 0; z < NS; ++z) {
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        sh[z][s] = sf[z][s][0][lane];
-        sl[z][s] = sf[z][s][1][lane];
-      }
-    }
-#pragma unroll
-    for (int z = 0; z < NS; ++z) X[z][0] = X[z][1] = f32x4{0, 0, 0, 0};
+    f16x8 sh[4], sl[4];
+    f32x4 X[2];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-#pragma unroll
-      for (int z = 0; z < NS; ++z) {
-        X[z][0] = mfma(as_frag(kf[s]), sh[z][s], X[z][0]);
-        X[z][1] = mfma(as_frag(kf[s]), sl[z][s], X[z][1]);
-      }
+      sh[s] = sf[s][0][lane];
+      sl[s] = sf[s][1][lane];
     }
+    X[0] = X[1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int z = 0; z < NS; ++z) {
+    for (int s = 0; s < 4; ++s) {
+      X[0] = mfma(as_frag(kf[s]), sh[s], X[0]);
+      X[1] = mfma(as_frag(kf[s]), sl[s], X[1]);
+    }
+    {
       f16x4 rh, rl;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         _Float16 vh, vl;
-        split16(fmaf(-as[z][r], X[z][0][r] + X[z][1][r], vs[z][r]), vh, vl);
+        split16(fmaf(-as[r], X[0][r] + X[1][r], vs[r]), vh, vl);
         rh[r] = vh;
         rl[r] = vl;
       }
-      rf[z][w >> 1][0][lane][w & 1] = rh;
-      rf[z][w >> 1][1][lane][w & 1] = rl;
+      rf[w >> 1][0][lane][w & 1] = rh;
+      rf[w >> 1][1][lane][w & 1] = rl;
     }
     load_keys(kn);
     __syncthreads();
     // T R and the D pair; Q S^T meanwhile
-    f16x8 rh[NS][2], rl[NS][2];
+    f16x8 rh[2], rl[2];
 #pragma unroll
-    for (int z = 0; z < NS; ++z) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s <= (w >> 1)) {
-          rh[z][s] = *reinterpret_cast<const f16x8*>(&rf[z][s][0][lane][0]);
-          rl[z][s] = *reinterpret_cast<const f16x8*>(&rf[z][s][1][lane][0]);
-        }
+    for (int s = 0; s < 2; ++s) {
+      if (s <= (w >> 1)) {
+        rh[s] = *reinterpret_cast<const f16x8*>(&rf[s][0][lane][0]);
+        rl[s] = *reinterpret_cast<const f16x8*>(&rf[s][1][lane][0]);
       }
     }
-    f32x4 Y[NS];
-#pragma unroll
-    for (int z = 0; z < NS; ++z) Y[z] = f32x4{0, 0, 0, 0};
+    f32x4 Y = {0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-#pragma unroll
-      for (int z = 0; z < NS; ++z) {
-        Y[z] = mfma(as_frag(qf[s]), sh[z][s], Y[z]);
-        Y[z] = mfma(as_frag(qf[s]), sl[z][s], Y[z]);
-      }
+      Y = mfma(as_frag(qf[s]), sh[s], Y);
+      Y = mfma(as_frag(qf[s]), sl[s], Y);
     }
-#pragma unroll
-    for (int z = 0; z < NS; ++z) {
+    {
       f32x4 D0 = {0, 0, 0, 0}, D1 = {0, 0, 0, 0};
-      D0 = mfma(as_frag(th[0]), rh[z][0], D0);
-      D1 = mfma(as_frag(tl[0]), rh[z][0], D1);
-      D0 = mfma(as_frag(th[0]), rl[z][0], D0);
+      D0 = mfma(as_frag(th[0]), rh[0], D0);
+      D1 = mfma(as_frag(tl[0]), rh[0], D1);
+      D0 = mfma(as_frag(th[0]), rl[0], D0);
       if (w >= 2) {
-        D1 = mfma(as_frag(tl[1]), rh[z][1], D1);
-        D0 = mfma(as_frag(th[1]), rh[z][1], D0);
-        D1 = mfma(as_frag(th[1]), rl[z][1], D1);
+        D1 = mfma(as_frag(tl[1]), rh[1], D1);
+        D0 = mfma(as_frag(th[1]), rh[1], D0);
+        D1 = mfma(as_frag(th[1]), rl[1], D1);
       }
       f16x4 dh, dl;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         _Float16 vh, vl;
-        split16((D0[r] + D1[r]) * fd[z], vh, vl);
+        split16((D0[r] + D1[r]) * fd, vh, vl);
         dh[r] = vh;
         dl[r] = vl;
       }
-      df[z][w >> 1][0][lane][w & 1] = dh;
-      df[z][w >> 1][1][lane][w & 1] = dl;
+      df[w >> 1][0][lane][w & 1] = dh;
+      df[w >> 1][1][lane][w & 1] = dl;
     }
-#pragma unroll
-    for (int z = 0; z < NS; ++z) {
-      const float ss = (ssum[z][0][n] + ssum[z][1][n]) + (ssum[z][2][n] + ssum[z][3][n]);
-      bound[z] = fmaf(cs1 * inv_s[z], __builtin_amdgcn_sqrtf(ss), bound[z]);
-    }
+    const float ss = (ssum[0][n] + ssum[1][n]) + (ssum[2][n] + ssum[3][n]);
+    bound = fmaf(cs1 * inv_s, __builtin_amdgcn_sqrtf(ss), bound);
     load_queries(kn);
     load_t(hn);
     if (more) prepare_values(c + 1, vnext);
     __syncthreads();
     // the new state; M R and the output meanwhile
-    f16x8 dh[NS][2], dl[NS][2];
+    f16x8 dh[2], dl[2];
 #pragma unroll
-    for (int z = 0; z < NS; ++z) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        dh[z][s] = *reinterpret_cast<const f16x8*>(&df[z][s][0][lane][0]);
-        dl[z][s] = *reinterpret_cast<const f16x8*>(&df[z][s][1][lane][0]);
-      }
+    for (int s = 0; s < 2; ++s) {
+      dh[s] = *reinterpret_cast<const f16x8*>(&df[s][0][lane][0]);
+      dl[s] = *reinterpret_cast<const f16x8*>(&df[s][1][lane][0]);
     }
-    f32x4 O[NS];
+    f32x4 O = mfma(as_frag(ml[0]), rh[0], f32x4{0, 0, 0, 0});
+    O = mfma(as_frag(mh[0]), rl[0], O);
+    O = mfma(as_frag(mh[0]), rh[0], O);
+    if (w >= 2) {
+      O = mfma(as_frag(ml[1]), rh[1], O);
+      O = mfma(as_frag(mh[1]), rl[1], O);
+      O = mfma(as_frag(mh[1]), rh[1], O);
+    }
+    f32x4 u[2];
 #pragma unroll
-    for (int z = 0; z < NS; ++z) {
-      O[z] = mfma(as_frag(ml[0]), rh[z][0], f32x4{0, 0, 0, 0});
-      O[z] = mfma(as_frag(mh[0]), rl[z][0], O[z]);
-      O[z] = mfma(as_frag(mh[0]), rh[z][0], O[z]);
-      if (w >= 2) {
-        O[z] = mfma(as_frag(ml[1]), rh[z][1], O[z]);
-        O[z] = mfma(as_frag(mh[1]), rl[z][1], O[z]);
-        O[z] = mfma(as_frag(mh[1]), rh[z][1], O[z]);
-      }
+    for (int m = 0; m < 2; ++m) {
+      u[m] = mfma(as_frag(kt[2 * m]), dh[0], f32x4{0, 0, 0, 0});
+      u[m] = mfma(as_frag(kt[2 * m]), dl[0], u[m]);
+      u[m] = mfma(as_frag(kt[2 * m + 1]), dh[1], u[m]);
+      u[m] = mfma(as_frag(kt[2 * m + 1]), dl[1], u[m]);
     }
 #pragma unroll
-    for (int z = 0; z < NS; ++z) {
-      f32x4 u[2];
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        u[m] = mfma(as_frag(kt[2 * m]), dh[z][0], f32x4{0, 0, 0, 0});
-        u[m] = mfma(as_frag(kt[2 * m]), dl[z][0], u[m]);
-        u[m] = mfma(as_frag(kt[2 * m + 1]), dh[z][1], u[m]);
-        u[m] = mfma(as_frag(kt[2 * m + 1]), dl[z][1], u[m]);
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) S[z][m][r] = fmaf(inv_d[z], u[m][r], gamma * S[z][m][r]);
-    }
+      for (int r = 0; r < 4; ++r) S[m][r] = fmaf(inv_d, u[m][r], gamma * S[m][r]);
     const float et[4] = {ev.x, ev.y, ev.z, ev.w}, rt[4] = {rv.x, rv.y, rv.z, rv.w};
     float* op = obase + static_cast<size_t>(c) * kBlock * row_el;
     const int left = t1 - (t0 + c * kBlock + 16 * w);   // uniform
+    float v[4];
 #pragma unroll
-    for (int z = 0; z < NS; ++z) {
-      if (row_ok[z]) {
-        float v[4];
+    for (int r = 0; r < 4; ++r) v[r] = rt[r] * fmaf(et[r] * inv_s, Y[r], fo * O[r]);
+    if (left >= 16) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = rt[r] * fmaf(et[r] * inv_s[z], Y[z][r], fo[z] * O[z][r]);
-        if (left >= 16) {
+      for (int r = 0; r < 4; ++r) *(op + r * row_el + el) = v[r];
+    } else {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) *(op + r * row_el + el[z]) = v[r];
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (4 * q + r < left) *(op + r * row_el + el[z]) = v[r];
-        }
-      }
+      for (int r = 0; r < 4; ++r)
+        if (4 * q + r < left) *(op + r * row_el + el) = v[r];
     }
     load_cols(kn);
     load_m(hn);
@@ -930,13 +886,8 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
     block(c, vb, va, sc1, sc0);
     if (++c == nblk) break;
   }
-#pragma unroll
-  for (int z = 0; z < NS; ++z) {
-    if (row_ok[z]) {
-      *reinterpret_cast<f32x4*>(sp[z]) = S[z][0];
-      *reinterpret_cast<f32x4*>(sp[z] + 16) = S[z][1];
-    }
-  }
+  *reinterpret_cast<f32x4*>(sp) = S[0];
+  *reinterpret_cast<f32x4*>(sp + 16) = S[1];
 }
 
 size_t prefill_bytes(const moe_gdn_desc* d, int N) {
@@ -944,22 +895,30 @@ size_t prefill_bytes(const moe_gdn_desc* d, int N) {
                      : prefill_slots(d->batch, N) * (d->k_heads * kKeyBytes + d->v_heads * kHeadBytes);
 }
 
+// Up to so many workgroups of 16 state rows (two for each compute unit) every
+// row has its own lanes: the chain of a token is shorter (16 tokens of 2
+// sequences with 32 heads of 128: 15.1 us against 18.8 with four rows to a
+// lane; of 4 sequences, past the limit: 22.6 against 20.6; of 64: 230 against 144).
+constexpr int kFewRows = 512;
+
 template <int ACT>
 hipError_t launch_prefill(const GdnArgs& a, uint8_t* ws, hipStream_t s) {
-  if (a.N <= kShort) {
-    hipLaunchKernelGGL(k_gdn_tokens<ACT>, dim3(a.Hv * (a.dv / 16), a.B), dim3(256), 0, s, a);
-    return hipGetLastError();
+  hipError_t e = hipSuccess;
+  if (a.N <= kShort || a.B > 1) {
+    const int rows = a.Hv * (a.dv / 16);
+    if (static_cast<int64_t>(rows) * a.B <= kFewRows)
+      hipLaunchKernelGGL((k_gdn_tokens<ACT, 1>), dim3(rows, a.B), dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_gdn_tokens<ACT, 4>), dim3(a.Hv * ((a.dv + 63) / 64), a.B), dim3(256), 0, s, a);
+    e = hipGetLastError();
   }
+  if (e != hipSuccess || a.N <= kShort) return e;
   hipLaunchKernelGGL(k_gdn_blocks<ACT>, dim3(static_cast<uint32_t>(prefill_slots(a.B, a.N)), a.Hv), dim3(256), 0, s, a,
                      ws);
-  hipError_t e = hipGetLastError();
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // 16 state rows per workgroup: with 32 the compiler keeps a block's operands
-  // in more registers than two waves per SIMD leave (516 against 325 us at 8192
-  // tokens with one wave per SIMD, 1270 us with spills)
-  constexpr int ns = 1;
-  const int units = a.Hv * ((a.dv + 16 * ns - 1) / (16 * ns)), run = (units + 7) / 8;
-  hipLaunchKernelGGL((k_gdn_scan<ACT, ns>), dim3(static_cast<uint32_t>(a.B) * 8 * run), dim3(256), 0, s, a, ws);
+  const int units = a.Hv * (a.dv / 16), run = (units + 7) / 8;
+  hipLaunchKernelGGL(k_gdn_scan<ACT>, dim3(static_cast<uint32_t>(a.B) * 8 * run), dim3(256), 0, s, a, ws);
   return hipGetLastError();
 }
 

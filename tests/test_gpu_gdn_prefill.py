@@ -172,6 +172,22 @@ def test_a_sequences_results_do_not_depend_on_the_batch():
         assert np.array_equal(o1, o[at[b]:at[b + 1]]) and np.array_equal(S1[0], S[b])
 
 
+@pytest.mark.parametrize("dv,act", [(48, "bf16"), (128, "f16")])
+def test_many_short_sequences_as_each_alone(dv, act):
+    # enough state rows that a lane takes several; lengths around the longest
+    # that goes token by token; rows of d_v past the last group of 64
+    lens = [(7 * i) % 26 for i in range(24)] + [90]
+    d, got = check(lens, 4, 8, dv, act, 23)
+    at = 0
+    for i, n in enumerate(lens):
+        one = {k: v[at:at + n] for k, v in d.items() if k != "state"}
+        one["state"] = d["state"][i:i + 1]
+        alone = gpu(one, [n], act)
+        assert np.array_equal(alone[0], got[0][at:at + n]), (i, n)
+        assert np.array_equal(alone[1][0], got[1][i]), (i, n)
+        at += n
+
+
 def test_continues_where_it_stopped_and_agrees_with_the_step():
     import torch
     from int4_routed_expert_router_amd import api
