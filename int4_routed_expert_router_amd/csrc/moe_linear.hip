@@ -63,7 +63,14 @@ constexpr int kLinBatch = 4;    // chunks whose loads a wave issues together
 
 // One workgroup: 32 weight rows (pair-tile blockIdx.x) x 16 TT tokens
 // (blockIdx.y).  The waves split the columns; their fp32 partial tiles are
-// added in wave order.
+// added in wave order.  A wave issues all loads of its next 4 chunks before it
+// uses one: with few tokens nothing else hides their latency.
+//
+// A vocabulary of 100003 rows, 2048 inputs, one token: 24 us, 115.6 MB at 4.8
+// TB/s, bound by reading the weights.  8192 outputs for one token (9.5 MB): 4.1
+// us in the kernel, bound by the latency of the launch, two dependent loads and the
+// join; 64 tokens of 2048 outputs: 4.7 us.  From about 512 workgroups on it is
+// bound by the conversions, which are repeated for every 16 TT tokens.
 template <int ACT, int RES, int TT, bool G32>
 __global__ __launch_bounds__(64 * kLinWaves) void k_linear(const uint8_t* __restrict__ packed,
                                                            const uint16_t* __restrict__ x, void* __restrict__ y, int T,
@@ -159,6 +166,11 @@ __global__ __launch_bounds__(64 * kLinWaves) void k_linear(const uint8_t* __rest
 // (b - 16 s) (sum x) term is added by fp32 matrix instructions (4 units deep),
 // which costs a quarter of the main products' matrix time and spares 64
 // multiply-adds a chunk.
+//
+// 499 tokens, 2048 inputs, 8192 outputs: 32 us, 525 TF/s.  Bound by one
+// workgroup's chain per compute unit: conversions, products and scalings of a
+// chunk add up where its two waves per SIMD do not overlap; with four waves (one
+// per SIMD, every chunk) it took 36 to 39 us.
 constexpr int kTileT = 128, kTileN = 128;
 // v + v of the lane that the DPP control names (one instruction)
 template <int kCtrl>
@@ -382,13 +394,26 @@ hipError_t launch_linear(const moe_linear_desc* d, const uint8_t* packed, const 
   const int K = d->in_dim, N = d->out_dim, G = d->group_size;
   const uint64_t off = padded_rows(N) * K / 2;
   const int np = (N + 31) / 32, nt = (T + kTileT - 1) / kTileT, nr = (N + kTileN - 1) / kTileN;
-  if (T > 64 && static_cast<int64_t>(nt) * nr >= 128) {
+  // The 128 x 128 tiles where there are enough of them to fill the chip half,
+  // k_linear otherwise (us, tiles against k_linear; 2048 inputs): 64 tiles
+  // 26.6 / 18.8 (512 tokens, 2048 outputs) and 26.4 / 18.6 (128 tokens, 8192);
+  // 128 tiles 27.4 / 34.6, 27.5 / 34.5 and 30.3 / 35.4 (4096 tokens, 512
+  // outputs).  Up to 64 tokens half of a tile's tokens are padding, which only
+  // pays when k_linear is bound by arithmetic: 64 tokens 26 / 19 with 128
+  // tiles, 51 / 67 with 512, 125 / 154 with 1187; 48 tokens 51 / 56 and 124 /
+  // 127; 32 tokens 50 / 35 and 123 / 78.
+  if (T > 48 && static_cast<int64_t>(nt) * nr >= (T > 64 ? 128 : 512)) {
     const dim3 grid((nr + 7) / 8 * 8 * nt), block(512);
     if (G == 32) hipLaunchKernelGGL((k_linear_tile<ACT, RES, true>), grid, block, 0, s, packed, x, y, T, N, K, G, off);
     else hipLaunchKernelGGL((k_linear_tile<ACT, RES, false>), grid, block, 0, s, packed, x, y, T, N, K, G, off);
     return hipGetLastError();
   }
   const int tiles = (T + 15) / 16;
+  // 16 tokens to a workgroup up to two workgroups for each compute unit, then
+  // 32, which convert a weight half as often (us, 16 against 32; 2048 inputs):
+  // 512 workgroups of 16 tokens 6.6 / 6.8 (128 tokens, 2048 outputs) and 6.4 /
+  // 6.6 (32 tokens, 8192), 320 of them 6.4 / 6.5, 256 of them 4.7 / 6.5; 1024
+  // of them 11.2 / 10.7 and 10.9 / 10.4.
   const int tt = tiles == 1 || static_cast<int64_t>(np) * tiles <= 512 ? 1 : 2;
   const dim3 grid(np, (tiles + tt - 1) / tt), block(64 * kLinWaves);
 #define LIN(TT)                                                                                             \
