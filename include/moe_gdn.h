@@ -70,7 +70,8 @@ moe_status moe_gdn_step(const moe_gdn_desc* desc, const void* q, const void* k, 
  * results do not depend on the other sequences.  g <= 0 is expected (any g
  * whose sums stay in fp32's exponent range works; -inf clears the state); a
  * non-finite k, v, beta or g makes that sequence's results unusable from the
- * start of its 64-token block on. */
+ * start of its 64-token block on.  A row of q or k whose sum of squares
+ * overflows fp32 counts as zero. */
 moe_status moe_gdn_prefill_workspace_bytes(const moe_gdn_desc* desc, int32_t n_tokens, size_t* bytes);
 moe_status moe_gdn_prefill(const moe_gdn_desc* desc, const int32_t* seq_off, int32_t n_tokens, const void* q,
                            const void* k, const void* v, const float* g, const float* beta, float q_scale,

@@ -7,7 +7,8 @@
  *
  * with q in 0..15 and fp16 s, b in groups of G inputs, as for the experts
  * (moe.h).  Products of x and q are exact and sums are fp32 in a fixed order
- * (bitwise repeatable); each output is rounded once to out_dtype.
+ * (bitwise repeatable) that depends on n_tokens: a token's results may differ in
+ * their last bits between batches.  Each output is rounded once to out_dtype.
  *
  * Weights are laid out once on the device by moe_linear_pack.  A value
  * outside a type's range overflows to infinity as a conversion does; a

@@ -284,7 +284,7 @@ __device__ __forceinline__ f32x4 mul16(float4 x, f32x4 y, f32x4 acc) {
 // side by side on other compute units, and the loads come from L2.
 //
 // 8192 tokens, 16 key and 32 value heads: 80 us for 4096 workgroups, four to a
-// compute unit; 300 MB of operands written at 3.8 TB/s.  A lone workgroup takes
+// compute unit; 205 MB of operands written at 2.6 TB/s.  A lone workgroup takes
 // about 9 us: loads and norms a quarter, k.k and q.k with their decays a fifth,
 // the inverse an eighth, T and M a fifth, scaling and stores the rest.
 template <int ACT>

@@ -152,6 +152,18 @@ def test_magnitudes(act, ks, vs, ss):
         close(got[1][:, :, dvi], want[1][:, :, dvi], f"state {dvi}")
 
 
+@pytest.mark.parametrize("lens", [[9], [90]], ids=["short", "blocks"])
+def test_rows_whose_squares_overflow_count_as_zero(lens):
+    d = inputs(lens, 1, 2, 32, "bf16", 31)
+    zero = {k: v.clone() for k, v in d.items()}
+    for key, rows in (("k", slice(2, None, 7)), ("q", slice(3, None, 5))):
+        d[key][rows] = 1e25
+        zero[key][rows] = 0
+    got, want = gpu(d, lens, "bf16"), ref(zero, lens)
+    close(got[0], want[0], "o")
+    close(got[1], want[1], "state")
+
+
 def test_full_size_layer_long_and_ragged():
     # the listed sizes' heads; checked on one key head's value heads at a time
     # would hide the others, so the oracle runs on every head of a shorter batch

@@ -44,6 +44,7 @@ CASES = [  # T, K, N, G, act, res
     # many rows: the tiles of 128 tokens x 128 rows
     (70, 192, 16400, 64, "bf16", "f32"), (257, 64, 5600, 32, "f16", "f16"), (130, 640, 8300, 128, "f16", "f32"),
     (385, 320, 4200, 32, "bf16", "bf16"), (128, 1152, 16385, 128, "bf16", "f32"), (65, 576, 16300, 64, "f16", "f32"),
+    (49, 128, 65440, 64, "f16", "bf16"), (64, 64, 65500, 32, "bf16", "f32"),
 ]
 IDS = ["T%d_K%d_N%d_G%d_%s_%s" % c for c in CASES]
 
