@@ -276,19 +276,19 @@ __device__ __forceinline__ f32x4 mul16(float4 x, f32x4 y, f32x4 acc) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(x.w, y[3], acc, 0, 0, 0);
 }
 
-// One workgroup per (slot, value head); wave w owns tile row w of the 64 x 64
-// products k.k and q.k, then tile column w of T and M.  The inverse is by
-// forward substitution (16 x 16 diagonal blocks column by column, then block
-// by block), which stays accurate also where powers of A grow.  A key head's
-// rows are loaded and multiplied once for each of its value heads: those run
-// side by side on other compute units, and the loads come from L2.
+// One workgroup per (slot, `per` value heads of a key head, one after the
+// other); wave w owns tile row w of the 64 x 64 products k.k and q.k, then tile
+// column w of T and M.  The inverse is by forward substitution (16 x 16 diagonal
+// blocks column by column, then block by block), which stays accurate also
+// where powers of A grow.
 //
-// 8192 tokens, 16 key and 32 value heads: 80 us for 4096 workgroups, four to a
-// compute unit; 205 MB of operands written at 2.6 TB/s.  A lone workgroup takes
-// about 9 us: loads and norms a quarter, k.k and q.k with their decays a fifth,
-// the inverse an eighth, T and M a fifth, scaling and stores the rest.
+// 8192 tokens, 16 key and 32 value heads: 76 us (80 with one value head to a
+// workgroup), four workgroups to a compute unit; 205 MB of operands written at
+// 2.7 TB/s.  A lone workgroup with one value head takes about 9 us: loads and norms
+// a quarter, k.k and q.k with their decays a fifth, the inverse an eighth, T and
+// M a fifth, scaling and stores the rest.
 template <int ACT>
-__global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restrict__ ws) {
+__global__ __launch_bounds__(256, 4) void k_gdn_blocks(GdnArgs a, uint8_t* __restrict__ ws, int per) {
   __shared__ __attribute__((aligned(16))) uint16_t ks[kBlock * kRow];
   __shared__ __attribute__((aligned(16))) uint16_t qs[kBlock * kRow];
   __shared__ double Gs[kBlock];
@@ -297,9 +297,10 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
   __shared__ bool grows;   // some decay is above 1
   float* As = reinterpret_cast<float*>(ks);   // takes the place of the keys once their products are done
   float* Ps = reinterpret_cast<float*>(qs);
-  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, q = lane >> 4;
+  const int tid = threadIdx.x;
+  int lane = tid & 63, n = lane & 15, q = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int slot = blockIdx.x, h = blockIdx.y, rep = a.Hv / a.Hk, hk = h / rep;
+  const int slot = blockIdx.x, rep = a.Hv / a.Hk, h0 = blockIdx.y * per, hk = h0 / rep;
   int b, tok0, len;
   if (!find_block(a, slot, lane, b, tok0, len)) return;   // the same for every thread
 
@@ -341,26 +342,8 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
       }
     }
   }
-  float* vec = reinterpret_cast<float*>(ws + prefill_ws_heads(a) + (static_cast<size_t>(slot) * a.Hv + h) * kHeadBytes +
-                                        24 * 1024);
-  if (w == 0) {
-    // log decays are summed in fp64, in units of log 2: differences of sums far
-    // from 0 keep their digits (a block of strong decays reaches -1000 and
-    // below).  -inf counts as -1000, which clears the state just as well
-    // (e^-1000 = 0 in fp32).
-    const size_t at = static_cast<size_t>(tok0 + min(lane, len - 1)) * a.Hv + h;
-    const bool ok = lane < len;
-    float gt = ok ? a.g[at] : 0.0f;
-    gt = gt < -1000.0f ? -1000.0f : gt;
-    Gs[lane] = scan_f64(static_cast<double>(gt) * 1.4426950408889634, lane);
-    bs[lane] = ok ? a.beta[at] : 0.0f;
-    // not from the sums, which may rise by a rounding where g is 0
-    const bool any = __ballot(gt > 0.0f) != 0ull;
-    if (lane == 0) grows = any;
-  }
   __syncthreads();
-  if (w == 0) lr[lane] = exp2_of(Gs[63] - Gs[lane]) * rks[lane];   // read after the next barrier
-  if (h % rep == 0) {   // the key head's operands, once
+  if (h0 % rep == 0) {   // the key head's operands, once
     uint4* out = reinterpret_cast<uint4*>(ws + (static_cast<size_t>(slot) * a.Hk + hk) * kKeyBytes);
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
@@ -398,182 +381,207 @@ __global__ __launch_bounds__(256) void k_gdn_blocks(GdnArgs a, uint8_t* __restri
       }
     }
   }
-  __syncthreads();
-  // the lane's rows and columns, read before the products are stored (the
-  // compiler would read them again after every store)
-  double Gt[4], Gc[4];
-  float bt[4], rc[4];
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int t = 16 * w + 4 * q + r;
-    Gt[r] = Gs[t];
-    bt[r] = bs[t] * rks[t];
-    Gc[r] = Gs[16 * r + n];
-    rc[r] = rks[16 * r + n];
-  }
-  f32x4 diag = {0, 0, 0, 0};   // A's diagonal block w
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (j <= w) {
-      const int c = 16 * j + n;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * w + 4 * q + r;
-        const float e = exp2_of(Gt[r] - Gc[j]) * rc[j];
-        const float av = c < t ? bt[r] * e * kk[j][r] : 0.0f;
-        if (j < w) As[t * kRowF + c] = av;
-        else diag[r] = av;
-        Ps[t * kRowF + c] = c <= t ? e * qk[j][r] : 0.0f;
-      }
+  // from here on per value head; the barriers of one head's turn also part its
+  // use of the shared arrays from the next one's
+  for (int h = h0; h < h0 + per; ++h) {
+    // opaque: or the compiler keeps every address and mask of the body in
+    // registers across the turns, which leaves room for two workgroups only
+    asm volatile("" : "+v"(lane), "+v"(n), "+v"(q));
+    float* vec = reinterpret_cast<float*>(ws + prefill_ws_heads(a) + (static_cast<size_t>(slot) * a.Hv + h) * kHeadBytes +
+                                          24 * 1024);
+    if (w == 0) {
+      // log decays are summed in fp64, in units of log 2: differences of sums far
+      // from 0 keep their digits (a block of strong decays reaches -1000 and
+      // below).  -inf counts as -1000, which clears the state just as well
+      // (e^-1000 = 0 in fp32).
+      const size_t at = static_cast<size_t>(tok0 + min(lane, len - 1)) * a.Hv + h;
+      const bool ok = lane < len;
+      float gt = ok ? a.g[at] : 0.0f;
+      gt = gt < -1000.0f ? -1000.0f : gt;
+      Gs[lane] = scan_f64(static_cast<double>(gt) * 1.4426950408889634, lane);
+      bs[lane] = ok ? a.beta[at] : 0.0f;
+      // not from the sums, which may rise by a rounding where g is 0
+      const bool any = __ballot(gt > 0.0f) != 0ull;
+      if (lane == 0) grows = any;
     }
-  }
-  // column n of the inverse of I + diagonal block w (the four lane groups
-  // alike): x starts as column n of I; then for j = 0, 1, ...: x_i -= A_ij x_j
-  // for all i > j at once, A_ij taken from the lane that has it
-  f32x4 tcol[4];
-  {
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = i == n ? 1.0f : 0.0f;
-#pragma unroll
-    for (int j = 0; j < 15; ++j) {
-#pragma unroll
-      for (int i = j + 1; i < 16; ++i) {
-        const float aij = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(
-            static_cast<int>(__float_as_uint(diag[i & 3])), 16 * (i >> 2) + j)));
-        x[i] = fmaf(-aij, x[j], x[i]);
-      }
-      __builtin_amdgcn_sched_barrier(0);   // keeps the column's 15 scalars at most alive
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) tcol[0][r] = q == 0 ? x[r] : q == 1 ? x[4 + r] : q == 2 ? x[8 + r] : x[12 + r];
-  }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) As[(16 * w + 4 * q + r) * kRowF + 16 * w + n] = tcol[0][r];
-  __syncthreads();
-  if (w == 3) {   // the wave with the fewest blocks of T and M: the block's vectors and scalars
-    const double G = Gs[lane], last = Gs[63];
-    const float bt = bs[lane], eg = exp2_of(G), left = exp2_of(last - G);
-    vec[lane] = eg * rks[lane];
-    vec[64 + lane] = eg;
-    vec[128 + lane] = rqs[lane];
-    // bounds on what the block makes of a state row of norm s and values up to
-    // v (per state row), for the scales of the pairs: |R| <= v + gmax s,
-    // |e^(G_last - G) rk D| <= d0 v + d1 s, |S'| <= s0 v + s1 s.  The factors
-    // I - beta k k^T have norm max(1, |1 - beta|), rk <= 2^-12 (rows are scaled
-    // to a largest value of 2^12 or more).  With beta in [0, 2] and g <= 0,
-    // rho = rmax = 1 and gmax <= 1.
-    const float gmax = wave_max(eg), bmax = wave_max(fabsf(bt));
-    const float rho = __uint_as_float(wave_allreduce_u32(
-        __float_as_uint(fmaxf(1.0f, fabsf(1.0f - bt))),
-        [](uint32_t x, uint32_t y) { return __float_as_uint(__uint_as_float(x) * __uint_as_float(y)); }));
-    const float up = wave_max(static_cast<float>(G)), dn = -wave_max(-static_cast<float>(G));
-    const float rmax = grows ? __builtin_amdgcn_exp2f(fmaxf(up, 0.0f) - fminf(dn, 0.0f)) : 1.0f;
-    const float sb = wave_sum(fabsf(bt)) * rmax, sg = wave_sum(fabsf(bt) * left);
-    const float dd = bmax * rmax * 0x1p-12f, gamma = exp2_of(last);
-    if (lane == 0) {
-      vec[kScGamma] = gamma;
-      vec[kScGmax] = gmax;
-      vec[kScD0] = dd * (1.0f + rho * sb);
-      vec[kScD1] = dd * rho * gmax;
-      vec[kScS0] = rho * sg;
-      vec[kScS1] = rho * gamma;
-    }
-  }
-  auto rows = [&](const float* m, int i, int k) {   // operand rows of block (i, k)
-    return *reinterpret_cast<const float4*>(m + (16 * i + n) * kRowF + 16 * k + 4 * q);
-  };
-#pragma unroll
-  for (int d = 1; d < 4; ++d) {
-    tcol[d] = f32x4{0, 0, 0, 0};
-    if (w + d < 4) {
-      f32x4 acc = {0, 0, 0, 0};
-#pragma unroll
-      for (int e = 0; e < d; ++e) acc = mul16(rows(As, w + d, w + e), tcol[e], acc);
-      const f32x4 t = mul16(rows(As, w + d, w + d), acc, f32x4{0, 0, 0, 0});
-      tcol[d] = -t;
-    }
-  }
-  f32x4 mcol[4];
-  float tm = 0.0f, mm = 0.0f;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    mcol[d] = f32x4{0, 0, 0, 0};
-    if (w + d < 4) {
-#pragma unroll
-      for (int e = 0; e <= d; ++e) mcol[d] = mul16(rows(Ps, w + d, w + e), tcol[e], mcol[d]);
-    }
-  }
-  const float bc = bs[16 * w + n];
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    if (w + d < 4) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int t = 16 * (w + d) + 4 * q + r;
-        tcol[d][r] *= bc * lr[t];
-        mcol[d][r] *= bc;
-        // a non-finite query row must not set the scale of the others
-        const float at = fabsf(tcol[d][r]), am = fabsf(mcol[d][r]);
-        tm = fmaxf(tm, at <= 3e38f ? at : 0.0f);
-        mm = fmaxf(mm, am <= 3e38f ? am : 0.0f);
-      }
-    }
-  }
-  tm = wave_max(tm);
-  mm = wave_max(mm);
-  if (lane == 0) {
-    wmax[w][0] = tm;
-    wmax[w][1] = mm;
-  }
-  __syncthreads();
-  const Pow2 pt = pow2_scale(fmaxf(fmaxf(wmax[0][0], wmax[1][0]), fmaxf(wmax[2][0], wmax[3][0])));
-  const Pow2 pm = pow2_scale(fmaxf(fmaxf(wmax[0][1], wmax[1][1]), fmaxf(wmax[2][1], wmax[3][1])));
-  if (tid == 0) {
-    vec[kScInvT] = pt.down;
-    vec[kScInvM] = pm.down;
-  }
-#pragma unroll
-  for (int d = 0; d < 4; ++d) {
-    if (w + d < 4) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int at = (16 * (w + d) + 4 * q + r) * kRowF + 16 * w + n;
-        As[at] = tcol[d][r] * pt.up;
-        Ps[at] = mcol[d][r] * pm.up;
-      }
-    }
-  }
-  if (w & 1) {   // blocks (0, 1) and (2, 3) lie above the diagonal, inside a stored step
+    __syncthreads();
+    if (w == 0) lr[lane] = exp2_of(Gs[63] - Gs[lane]) * rks[lane];   // read after the next barrier
+    // the lane's rows and columns, read before the products are stored (the
+    // compiler would read them again after every store)
+    double Gt[4], Gc[4];
+    float bt[4], rc[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int at = (16 * (w - 1) + 4 * q + r) * kRowF + 16 * w + n;
-      As[at] = 0.0f;
-      Ps[at] = 0.0f;
+      const int t = 16 * w + 4 * q + r;
+      Gt[r] = Gs[t];
+      bt[r] = bs[t] * rks[t];
+      Gc[r] = Gs[16 * r + n];
+      rc[r] = rks[16 * r + n];
     }
-  }
-  __syncthreads();
-  uint8_t* hd = ws + prefill_ws_heads(a) + (static_cast<size_t>(slot) * a.Hv + h) * kHeadBytes;
+    f32x4 diag = {0, 0, 0, 0};   // A's diagonal block w
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    if (s <= (w >> 1)) {
-      const int f = w < 2 ? w : 2 * w - 2 + s;
+    for (int j = 0; j < 4; ++j) {
+      if (j <= w) {
+        const int c = 16 * j + n;
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        const float* src = (m ? Ps : As) + (16 * w + n) * kRowF + 32 * s + 4 * q;
-        const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 16);
-        const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        f16x8 hi, lo;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          _Float16 vh, vl;
-          split16(v[j], vh, vl);
-          hi[j] = vh;
-          lo[j] = vl;
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * w + 4 * q + r;
+          const float e = exp2_of(Gt[r] - Gc[j]) * rc[j];
+          const float av = c < t ? bt[r] * e * kk[j][r] : 0.0f;
+          if (j < w) As[t * kRowF + c] = av;
+          else diag[r] = av;
+          Ps[t * kRowF + c] = c <= t ? e * qk[j][r] : 0.0f;
         }
-        f16x8* out = reinterpret_cast<f16x8*>(hd + m * 12 * 1024 + f * 2048) + lane;
-        out[0] = hi;
-        out[64] = lo;
+      }
+    }
+    // column n of the inverse of I + diagonal block w (the four lane groups
+    // alike): x starts as column n of I; then for j = 0, 1, ...: x_i -= A_ij x_j
+    // for all i > j at once, A_ij taken from the lane that has it
+    f32x4 tcol[4];
+    {
+      float x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = i == n ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 15; ++j) {
+#pragma unroll
+        for (int i = j + 1; i < 16; ++i) {
+          const float aij = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(
+              static_cast<int>(__float_as_uint(diag[i & 3])), 16 * (i >> 2) + j)));
+          x[i] = fmaf(-aij, x[j], x[i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);   // keeps the column's 15 scalars at most alive
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) tcol[0][r] = q == 0 ? x[r] : q == 1 ? x[4 + r] : q == 2 ? x[8 + r] : x[12 + r];
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) As[(16 * w + 4 * q + r) * kRowF + 16 * w + n] = tcol[0][r];
+    __syncthreads();
+    if (w == 3) {   // the wave with the fewest blocks of T and M: the block's vectors and scalars
+      const double G = Gs[lane], last = Gs[63];
+      const float bt = bs[lane], eg = exp2_of(G), left = exp2_of(last - G);
+      vec[lane] = eg * rks[lane];
+      vec[64 + lane] = eg;
+      vec[128 + lane] = rqs[lane];
+      // bounds on what the block makes of a state row of norm s and values up to
+      // v (per state row), for the scales of the pairs: |R| <= v + gmax s,
+      // |e^(G_last - G) rk D| <= d0 v + d1 s, |S'| <= s0 v + s1 s.  The factors
+      // I - beta k k^T have norm max(1, |1 - beta|), rk <= 2^-12 (rows are scaled
+      // to a largest value of 2^12 or more).  With beta in [0, 2] and g <= 0,
+      // rho = rmax = 1 and gmax <= 1.
+      const float gmax = wave_max(eg), bmax = wave_max(fabsf(bt));
+      const float rho = __uint_as_float(wave_allreduce_u32(
+          __float_as_uint(fmaxf(1.0f, fabsf(1.0f - bt))),
+          [](uint32_t x, uint32_t y) { return __float_as_uint(__uint_as_float(x) * __uint_as_float(y)); }));
+      const float up = wave_max(static_cast<float>(G)), dn = -wave_max(-static_cast<float>(G));
+      const float rmax = grows ? __builtin_amdgcn_exp2f(fmaxf(up, 0.0f) - fminf(dn, 0.0f)) : 1.0f;
+      const float sb = wave_sum(fabsf(bt)) * rmax, sg = wave_sum(fabsf(bt) * left);
+      const float dd = bmax * rmax * 0x1p-12f, gamma = exp2_of(last);
+      if (lane == 0) {
+        vec[kScGamma] = gamma;
+        vec[kScGmax] = gmax;
+        vec[kScD0] = dd * (1.0f + rho * sb);
+        vec[kScD1] = dd * rho * gmax;
+        vec[kScS0] = rho * sg;
+        vec[kScS1] = rho * gamma;
+      }
+    }
+    auto rows = [&](const float* m, int i, int k) {   // operand rows of block (i, k)
+      return *reinterpret_cast<const float4*>(m + (16 * i + n) * kRowF + 16 * k + 4 * q);
+    };
+#pragma unroll
+    for (int d = 1; d < 4; ++d) {
+      tcol[d] = f32x4{0, 0, 0, 0};
+      if (w + d < 4) {
+        f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < d; ++e) acc = mul16(rows(As, w + d, w + e), tcol[e], acc);
+        const f32x4 t = mul16(rows(As, w + d, w + d), acc, f32x4{0, 0, 0, 0});
+        tcol[d] = -t;
+      }
+    }
+    f32x4 mcol[4];
+    float tm = 0.0f, mm = 0.0f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      mcol[d] = f32x4{0, 0, 0, 0};
+      if (w + d < 4) {
+#pragma unroll
+        for (int e = 0; e <= d; ++e) mcol[d] = mul16(rows(Ps, w + d, w + e), tcol[e], mcol[d]);
+      }
+    }
+    const float bc = bs[16 * w + n];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      if (w + d < 4) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int t = 16 * (w + d) + 4 * q + r;
+          tcol[d][r] *= bc * lr[t];
+          mcol[d][r] *= bc;
+          // a non-finite query row must not set the scale of the others
+          const float at = fabsf(tcol[d][r]), am = fabsf(mcol[d][r]);
+          tm = fmaxf(tm, at <= 3e38f ? at : 0.0f);
+          mm = fmaxf(mm, am <= 3e38f ? am : 0.0f);
+        }
+      }
+    }
+    tm = wave_max(tm);
+    mm = wave_max(mm);
+    if (lane == 0) {
+      wmax[w][0] = tm;
+      wmax[w][1] = mm;
+    }
+    __syncthreads();
+    const Pow2 pt = pow2_scale(fmaxf(fmaxf(wmax[0][0], wmax[1][0]), fmaxf(wmax[2][0], wmax[3][0])));
+    const Pow2 pm = pow2_scale(fmaxf(fmaxf(wmax[0][1], wmax[1][1]), fmaxf(wmax[2][1], wmax[3][1])));
+    if (tid == 0) {
+      vec[kScInvT] = pt.down;
+      vec[kScInvM] = pm.down;
+    }
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      if (w + d < 4) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int at = (16 * (w + d) + 4 * q + r) * kRowF + 16 * w + n;
+          As[at] = tcol[d][r] * pt.up;
+          Ps[at] = mcol[d][r] * pm.up;
+        }
+      }
+    }
+    if (w & 1) {   // blocks (0, 1) and (2, 3) lie above the diagonal, inside a stored step
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int at = (16 * (w - 1) + 4 * q + r) * kRowF + 16 * w + n;
+        As[at] = 0.0f;
+        Ps[at] = 0.0f;
+      }
+    }
+    __syncthreads();
+    uint8_t* hd = ws + prefill_ws_heads(a) + (static_cast<size_t>(slot) * a.Hv + h) * kHeadBytes;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (s <= (w >> 1)) {
+        const int f = w < 2 ? w : 2 * w - 2 + s;
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const float* src = (m ? Ps : As) + (16 * w + n) * kRowF + 32 * s + 4 * q;
+          const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 16);
+          const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          f16x8 hi, lo;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            _Float16 vh, vl;
+            split16(v[j], vh, vl);
+            hi[j] = vh;
+            lo[j] = vl;
+          }
+          f16x8* out = reinterpret_cast<f16x8*>(hd + m * 12 * 1024 + f * 2048) + lane;
+          out[0] = hi;
+          out[64] = lo;
+        }
       }
     }
   }
@@ -918,6 +926,13 @@ size_t prefill_bytes(const moe_gdn_desc* d, int N) {
 // sequences with 32 heads of 128: 15.1 us against 18.8 with four rows to a
 // lane; of 4 sequences, past the limit: 22.6 against 20.6; of 64: 230 against 144).
 constexpr int kFewRows = 512;
+// From so many blocks (slots x value heads) on, a workgroup of k_gdn_blocks
+// takes two value heads of a key head, which share its loads and products; below,
+// the turns only lengthen the kernel's tail (us in all, two against one; 16 key
+// and 32 value heads of 128): 8192 tokens (4128 blocks) 307 / 319, 8 x 512 tokens
+// (2304) 123 / 119, 4096 tokens (2080) 136 / 140, 8 x 256 (1280) 77 / 74, 2048
+// tokens (1056) 80 / 76.
+constexpr int kManyBlocks = 4096;
 
 template <int ACT>
 hipError_t launch_prefill(const GdnArgs& a, uint8_t* ws, hipStream_t s) {
@@ -931,8 +946,9 @@ hipError_t launch_prefill(const GdnArgs& a, uint8_t* ws, hipStream_t s) {
     e = hipGetLastError();
   }
   if (e != hipSuccess || a.N <= kShort) return e;
-  hipLaunchKernelGGL(k_gdn_blocks<ACT>, dim3(static_cast<uint32_t>(prefill_slots(a.B, a.N)), a.Hv), dim3(256), 0, s, a,
-                     ws);
+  const auto slots = static_cast<uint32_t>(prefill_slots(a.B, a.N));
+  const int per = a.Hv / a.Hk % 2 == 0 && static_cast<int64_t>(slots) * a.Hv >= kManyBlocks ? 2 : 1;
+  hipLaunchKernelGGL(k_gdn_blocks<ACT>, dim3(slots, a.Hv / per), dim3(256), 0, s, a, ws, per);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int units = a.Hv * (a.dv / 16), run = (units + 7) / 8;

@@ -152,6 +152,23 @@ def test_magnitudes(act, ks, vs, ss):
         close(got[1][:, :, dvi], want[1][:, :, dvi], f"state {dvi}")
 
 
+@pytest.mark.parametrize("hk", [16, 64])
+def test_many_blocks_as_each_alone(hk):
+    # so many blocks that one workgroup prepares two value heads of a key head
+    # (with four or one value heads each)
+    lens = [25 + 9 * (i % 5) for i in range(50)]
+    d, got = check(lens, hk, 64, 16, "bf16", 41)
+    at = 0
+    for i, n in enumerate(lens):
+        if i % 7 == 0:
+            one = {k: v[at:at + n] for k, v in d.items() if k != "state"}
+            one["state"] = d["state"][i:i + 1]
+            alone = gpu(one, [n], "bf16")
+            assert np.array_equal(alone[0], got[0][at:at + n]), (i, n)
+            assert np.array_equal(alone[1][0], got[1][i]), (i, n)
+        at += n
+
+
 @pytest.mark.parametrize("lens", [[9], [90]], ids=["short", "blocks"])
 def test_rows_whose_squares_overflow_count_as_zero(lens):
     d = inputs(lens, 1, 2, 32, "bf16", 31)
