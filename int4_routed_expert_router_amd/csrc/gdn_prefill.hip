@@ -679,8 +679,8 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
     th[0] = frag(p, 0);
     tl[0] = frag(p, 1024);
     if (w >= 2) {
-      th[1] = frag(p, 2048);
-      tl[1] = frag(p, 3072);
+      th[1] = frag(p, 2 * 1024);
+      tl[1] = frag(p, 3 * 1024);
     }
   };
   auto load_m = [&](const uint8_t* ph) {
@@ -688,8 +688,8 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
     mh[0] = frag(p, 0);
     ml[0] = frag(p, 1024);
     if (w >= 2) {
-      mh[1] = frag(p, 2048);
-      ml[1] = frag(p, 3072);
+      mh[1] = frag(p, 2 * 1024);
+      ml[1] = frag(p, 3 * 1024);
     }
     ev = vec4(ph, 256);
     rv = vec4(ph, 512);
