@@ -782,10 +782,13 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
       inv_d = pd.down;
       bound = cs0 * vm;   // the next block's, completed below
       const float at[4] = {sc.eg.x, sc.eg.y, sc.eg.z, sc.eg.w};
+      // the two scales' product overflows only where every e^G of the block is
+      // below fp32's normal numbers (and v is 0): a finite factor keeps 0 x it 0
+      const float sr = fminf(inv_s * pr.up, 0x1.fffffep127f);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         vs[r] = act_to_f32<ACT>(vv[r]) * pr.up;
-        as[r] = at[r] * (inv_s * pr.up);
+        as[r] = at[r] * sr;
       }
     }
     __syncthreads();
