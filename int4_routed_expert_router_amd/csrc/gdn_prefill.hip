@@ -169,10 +169,10 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 //   per (slot, key head):   K rows [4 tiles][4 steps], Q rows the same, K columns [8 tiles][2 steps]
 //   per (slot, value head): T and M rows as [6][hi, lo] (tile rows 0, 1: step 0; 2, 3: steps 0 and 1),
 //                           256 floats: e^G rk, e^G, rq per token, then kSc*
+// Of a block that goes token by token (see k_gdn_scan) only kScGamma is set, to -1.
 constexpr size_t kKeyBytes = 48 * 1024;
 constexpr size_t kHeadBytes = 25 * 1024;
-constexpr int kScGamma = 192, kScInvT = 193, kScInvM = 194, kScGmax = 195, kScD0 = 196, kScD1 = 197, kScS0 = 198,
-              kScS1 = 199;
+constexpr int kScGamma = 192, kScInvT = 193, kScInvM = 194, kScGmax = 195, kScD0 = 196, kScD1 = 197, kScS0 = 198;
 
 __host__ __device__ inline size_t prefill_slots(int B, int N) { return static_cast<size_t>(N) / kBlock + B; }
 
@@ -294,7 +294,7 @@ __global__ __launch_bounds__(256, 4) void k_gdn_blocks(GdnArgs a, uint8_t* __res
   __shared__ double Gs[kBlock];
   __shared__ float bs[kBlock], rks[kBlock], rqs[kBlock], lr[kBlock];   // lr: e^(G_last - G) rk
   __shared__ float wmax[4][2];
-  __shared__ bool grows;   // some decay is above 1
+  __shared__ int rises;   // some g is above 0, or some beta outside [0, 2]
   float* As = reinterpret_cast<float*>(ks);   // takes the place of the keys once their products are done
   float* Ps = reinterpret_cast<float*>(qs);
   const int tid = threadIdx.x;
@@ -399,12 +399,17 @@ __global__ __launch_bounds__(256, 4) void k_gdn_blocks(GdnArgs a, uint8_t* __res
       float gt = ok ? a.g[at] : 0.0f;
       gt = gt < -1000.0f ? -1000.0f : gt;
       Gs[lane] = scan_f64(static_cast<double>(gt) * 1.4426950408889634, lane);
-      bs[lane] = ok ? a.beta[at] : 0.0f;
-      // not from the sums, which may rise by a rounding where g is 0
-      const bool any = __ballot(gt > 0.0f) != 0ull;
-      if (lane == 0) grows = any;
+      const float bt = ok ? a.beta[at] : 0.0f;
+      bs[lane] = bt;
+      const bool any = __ballot(!(gt <= 0.0f && bt >= 0.0f && bt <= 2.0f)) != 0ull;   // NaN too
+      if (lane == 0) rises = any ? 1 : 0;
     }
     __syncthreads();
+    if (__builtin_amdgcn_readfirstlane(rises) != 0) {
+      if (tid == 0) vec[kScGamma] = -1.0f;
+      __syncthreads();   // before the next turn writes `rises`
+      continue;
+    }
     if (w == 0) lr[lane] = exp2_of(Gs[63] - Gs[lane]) * rks[lane];   // read after the next barrier
     // the lane's rows and columns, read before the products are stored (the
     // compiler would read them again after every store)
@@ -466,25 +471,18 @@ __global__ __launch_bounds__(256, 4) void k_gdn_blocks(GdnArgs a, uint8_t* __res
       vec[128 + lane] = rqs[lane];
       // bounds on what the block makes of a state row of norm s and values up to
       // v (per state row), for the scales of the pairs: |R| <= v + gmax s,
-      // |e^(G_last - G) rk D| <= d0 v + d1 s, |S'| <= s0 v + s1 s.  The factors
-      // I - beta k k^T have norm max(1, |1 - beta|), rk <= 2^-12 (rows are scaled
-      // to a largest value of 2^12 or more).  With beta in [0, 2] and g <= 0,
-      // rho = rmax = 1 and gmax <= 1.
-      const float gmax = wave_max(eg), bmax = wave_max(fabsf(bt));
-      const float rho = __uint_as_float(wave_allreduce_u32(
-          __float_as_uint(fmaxf(1.0f, fabsf(1.0f - bt))),
-          [](uint32_t x, uint32_t y) { return __float_as_uint(__uint_as_float(x) * __uint_as_float(y)); }));
-      const float up = wave_max(static_cast<float>(G)), dn = -wave_max(-static_cast<float>(G));
-      const float rmax = grows ? __builtin_amdgcn_exp2f(fmaxf(up, 0.0f) - fminf(dn, 0.0f)) : 1.0f;
-      const float sb = wave_sum(fabsf(bt)) * rmax, sg = wave_sum(fabsf(bt) * left);
-      const float dd = bmax * rmax * 0x1p-12f, gamma = exp2_of(last);
+      // |e^(G_last - G) rk D| <= d0 v + d1 s, |S'| <= s0 v + gamma s.  They hold
+      // because the factors e^g (I - beta k k^T) have norm 1 at most (g <= 0,
+      // beta in [0, 2]) and rk <= 2^-12 (rows are scaled to a largest value of
+      // 2^12 or more).
+      const float gmax = wave_max(eg), bmax = wave_max(bt), dd = bmax * 0x1p-12f;
+      const float sb = wave_sum(bt), sg = wave_sum(bt * left), gamma = exp2_of(last);
       if (lane == 0) {
         vec[kScGamma] = gamma;
         vec[kScGmax] = gmax;
-        vec[kScD0] = dd * (1.0f + rho * sb);
-        vec[kScD1] = dd * rho * gmax;
-        vec[kScS0] = rho * sg;
-        vec[kScS1] = rho * gamma;
+        vec[kScD0] = dd * (1.0f + sb);
+        vec[kScD1] = dd * gmax;
+        vec[kScS0] = sg;
       }
     }
     auto rows = [&](const float* m, int i, int k) {   // operand rows of block (i, k)
@@ -596,6 +594,12 @@ __global__ __launch_bounds__(256, 4) void k_gdn_blocks(GdnArgs a, uint8_t* __res
 // loaded as soon as the block before is done with theirs; loads return in
 // order, so the values, which are needed first, are loaded two blocks ahead.
 //
+// The scales of the pairs need bounds on R, D and S' before those are known.
+// With g <= 0 and beta in [0, 2] (what gates produce) they exist; in a block with
+// another g or beta a state may grow by any factor and no scale of a whole block
+// fits fp16.  From the first such block of a sequence and value head on, its
+// workgroups go token by token in fp32 (33 us for 64 tokens instead of 1.95).
+//
 // 16 state rows to a workgroup: a tile of the matrix instruction, and the most
 // workgroups.  With 32 rows a block's operands do not fit beside two tiles of
 // results (8192 tokens, 32 heads of 128: 516 us in all with one wave per SIMD
@@ -627,16 +631,27 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
   int t0, t1;
   seq_range(a, b, t0, t1);
   if (t0 == t1) return;
-  if (t1 - t0 <= kShort) {   // in a batch they are k_gdn_tokens'
-    if (a.B == 1) run_tokens<ACT, 1>(a, b, h, t0, t1, dv0 + (tid >> 4));
-    return;
-  }
+  if (t1 - t0 <= kShort && a.B != 1) return;   // k_gdn_tokens' part
   t0 = __builtin_amdgcn_readfirstlane(t0);
   t1 = __builtin_amdgcn_readfirstlane(t1);
   const int nblk = (t1 - t0 + kBlock - 1) / kBlock, slot0 = t0 / kBlock + b, hk = h / (a.Hv / a.Hk);
   const uint8_t* kp = ws + (static_cast<size_t>(slot0) * a.Hk + hk) * kKeyBytes;
   const uint8_t* hp = ws + prefill_ws_heads(a) + (static_cast<size_t>(slot0) * a.Hv + h) * kHeadBytes;
   const size_t kstep = a.Hk * kKeyBytes, hstep = a.Hv * kHeadBytes;
+  // blocks before the first that goes token by token, 64 at a time (a test in
+  // the blocks' loop makes it longer: 8192 tokens 358 us instead of 313)
+  int end = t1 - t0 <= kShort ? 0 : nblk;
+  for (int c = 0; c < end; c += 64) {
+    const size_t i = min(c + lane, nblk - 1);
+    const unsigned long long m =
+        __ballot(*reinterpret_cast<const float*>(hp + i * hstep + 24 * 1024 + 4 * kScGamma) < 0.0f);
+    if (m != 0) end = min(c + __ffsll(m) - 1, nblk);
+  }
+  end = __builtin_amdgcn_readfirstlane(end);
+  if (end == 0) {
+    run_tokens<ACT, 1>(a, b, h, t0, t1, dv0 + (tid >> 4));
+    return;
+  }
   // uniform bases and 32-bit lane offsets: rows 16w + 4q + r of a block
   const uint32_t row_el = static_cast<uint32_t>(a.Hv) * a.dv;
   const uint16_t* vbase = a.v + (static_cast<size_t>(t0 + 16 * w) * a.Hv + h) * a.dv;
@@ -649,7 +664,7 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
   uint16_t va[4], vb[4];   // values of even and odd blocks
   float4 ev, rv;
   struct Scalars {
-    float4 a, b;   // kScGamma .. kScGmax, kScD0 .. kScS1
+    float4 a, b;   // kScGamma .. kScGmax, kScD0 .. kScS0
     float4 eg;     // e^G rk of the lane's rows
   } sc0, sc1;      // of even and odd blocks
   const uint32_t lane16 = lane * 16;
@@ -747,12 +762,12 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
   __syncthreads();
 
   auto block = [&](int c, uint16_t (&vv)[4], uint16_t (&vnext)[4], const Scalars& sc, Scalars& scnext) {
-    const bool more = c + 1 < nblk;
+    const bool more = c + 1 < end;
     const uint8_t* kn = more ? kp + kstep : kp;
     const uint8_t* hn = more ? hp + hstep : hp;
     load_scalars(hn, scnext);
     const float gamma = sc.a.x, inv_t = sc.a.y, inv_m = sc.a.z, gmax = sc.a.w, cd0 = sc.b.x, cd1 = sc.b.y,
-                cs0 = sc.b.z, cs1 = sc.b.w;
+                cs0 = sc.b.z;
     float inv_s, fd, fo, inv_d, vs[4], as[4];
     // S pair
     {
@@ -857,7 +872,7 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
       df[w >> 1][1][lane][w & 1] = dl;
     }
     const float ss = (ssum[0][n] + ssum[1][n]) + (ssum[2][n] + ssum[3][n]);
-    bound = fmaf(cs1 * inv_s, __builtin_amdgcn_sqrtf(ss), bound);
+    bound = fmaf(gamma * inv_s, __builtin_amdgcn_sqrtf(ss), bound);
     load_queries(kn);
     load_t(hn);
     if (more) prepare_values(c + 1, vnext);
@@ -899,9 +914,11 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
 #pragma unroll
       for (int r = 0; r < 4; ++r) *(op + r * row_el + el) = v[r];
     } else {
+      uint32_t at = el;
+      asm volatile("" : "+v"(at));   // or the compiler keeps the rows' addresses in registers
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (4 * q + r < left) *(op + r * row_el + el) = v[r];
+        if (4 * q + r < left) op[r * row_el + at] = v[r];
     }
     load_cols(kn);
     load_m(hn);
@@ -911,12 +928,16 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
   };
   for (int c = 0;;) {
     block(c, va, vb, sc0, sc1);
-    if (++c == nblk) break;
+    if (++c == end) break;
     block(c, vb, va, sc1, sc0);
-    if (++c == nblk) break;
+    if (++c == end) break;
   }
   *reinterpret_cast<f32x4*>(sp) = S[0];
   *reinterpret_cast<f32x4*>(sp + 16) = S[1];
+  if (end < nblk) {
+    __syncthreads();   // the rows are stored in parts of other lanes
+    run_tokens<ACT, 1>(a, b, h, t0 + end * kBlock, t1, dv0 + (tid >> 4));
+  }
 }
 
 size_t prefill_bytes(const moe_gdn_desc* d, int N) {

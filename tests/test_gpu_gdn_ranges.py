@@ -76,3 +76,113 @@ def test_cleared_large_states_are_zero_not_nan(lens, size, g0):
     d["g"][64:65] = g0
     d["v"][..., ::3] = 0
     hold(d, lens, "bf16")
+
+
+def rising(edit, d, lens):
+    """Gives the inputs decays above 1 or a beta outside [0, 2]."""
+    import torch
+    g, n = d["g"], sum(lens)
+    t = torch.arange(n)
+    if edit.startswith("beta"):
+        b = float(edit[4:])
+        d["beta"][:] = b
+        g -= math.log(max(1.0, abs(1.0 - b)))   # so that nothing grows
+    elif edit == "one small rise":
+        g[:] = -0.2
+        g[n // 3] = 0.001
+    elif edit == "steady rise":
+        g[:] = 0.3
+    elif edit == "one block's rise":
+        g[:] = -0.01
+        g[64:128] = 1.0
+    elif edit == "up and down":
+        g[:] = torch.where(t % 40 < 20, 0.9, -1.1).float()[:, None]
+    else:
+        assert edit == "one beta"
+        d["beta"][n // 2, 1] = 2.5
+
+
+RISES = ["beta-0.5", "beta-0.01", "beta2.1", "beta2.25", "beta3", "beta-7", "one small rise", "steady rise",
+         "one block's rise", "up and down", "one beta"]
+
+
+@pytest.mark.parametrize("lens", LENS + [[70, 3, 0, 129, 64]], ids=IDS + ["batch"])
+@pytest.mark.parametrize("edit", RISES)
+def test_decays_above_one_and_any_beta(lens, edit):
+    d = inputs(lens, 2, 4, 48, "bf16", 13)
+    rising(edit, d, lens)
+    hold(d, lens, "bf16")
+
+
+@pytest.mark.parametrize("dv,act", [(16, "f16"), (128, "bf16"), (256, "bf16")])
+def test_rises_at_other_head_sizes(dv, act):
+    lens = [200]
+    d = inputs(lens, 1, 2, dv, act, 17)
+    d["g"][30, 0] = 0.5
+    d["beta"][100, 1] = -1.0
+    hold(d, lens, act)
+
+
+@pytest.mark.parametrize("at", [0, 63, 64, 140, 191, 199])
+def test_only_the_head_that_rises_is_touched(at):
+    # blocks, heads and sequences without a rise keep their results bit for bit
+    lens = [200, 100]
+    d = inputs(lens, 2, 4, 32, "bf16", 19)
+    clean = gpu(d, lens, "bf16")
+    d["g"][at, 2] = 0.25
+    o, S = gpu(d, lens, "bf16")
+    other = [0, 1, 3]
+    assert np.array_equal(o[:, other], clean[0][:, other]) and np.array_equal(S[:, other], clean[1][:, other])
+    first = at // 64 * 64   # the head's blocks before, and the other sequence
+    assert np.array_equal(o[:first, 2], clean[0][:first, 2])
+    assert np.array_equal(o[200:], clean[0][200:]) and np.array_equal(S[1], clean[1][1])
+    hold(d, lens, "bf16")
+
+
+def test_rises_in_a_batch_of_many_blocks_as_each_alone():
+    # so many blocks that one workgroup may prepare two value heads of a key head
+    lens = [25 + 9 * (i % 5) for i in range(50)]
+    d = inputs(lens, 16, 64, 16, "bf16", 23)
+    d["g"][3::50, ::3] = 0.1
+    d["beta"][7::40, 1::5] = 2.2
+    got = gpu(d, lens, "bf16")
+    at = 0
+    for i, n in enumerate(lens):
+        if i % 7 == 0:
+            one = {k: v[at:at + n] for k, v in d.items() if k != "state"}
+            one["state"] = d["state"][i:i + 1]
+            alone = gpu(one, [n], "bf16")
+            assert np.array_equal(alone[0], got[0][at:at + n]) and np.array_equal(alone[1][0], got[1][i])
+        at += n
+    hold({k: (v[:1] if k == "state" else v[:lens[0]]) for k, v in d.items()}, lens[:1], "bf16")
+
+
+def test_captured_with_rises_that_come_and_go():
+    import torch
+    from int4_routed_expert_router_amd import api
+    lens = [150, 40]
+    d = inputs(lens, 2, 4, 64, "bf16", 29)
+    c = {k: v.cuda() for k, v in d.items()}
+    off, s0, n = offsets(lens), c["state"].clone(), sum(lens)
+    ws = api.gdn_prefill_workspace(len(lens), n, 2, 4, 64)
+    o = [torch.empty(n, 4, 64, device="cuda") for _ in range(2)]
+    s = [s0.clone() for _ in range(2)]
+
+    def run(i):
+        api.gdn_prefill(c["q"], c["k"], c["v"], c["g"], c["beta"], s[i], o[i], off, Q_SCALE, "bf16", ws=ws)
+
+    run(0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(0)
+    for at in (None, 20, None, 100, 149):
+        c["g"].copy_(d["g"])
+        if at is not None:
+            c["g"][at] = 0.5
+        for x in s:
+            x.copy_(s0)
+        graph.replay()
+        torch.cuda.synchronize()
+        run(1)
+        torch.cuda.synchronize()
+        assert torch.equal(o[0], o[1]) and torch.equal(s[0], s[1])
