@@ -144,9 +144,16 @@ __global__ __launch_bounds__(256) void k_gdn_tokens(GdnArgs a) {
 // k_gdn_scan then takes one sequence's blocks in order.
 //
 // State and results are fp32, so fp32 operands enter the matrix cores as an
-// fp16 pair hi + lo (22 significant bits) under a power-of-two scale that
-// keeps them within fp16's range; keys and queries are exact in fp16 once each
-// row is scaled by a power of two (the row's norm is applied afterwards).
+// fp16 pair hi + lo / 2^11 (22 significant bits) under a power-of-two scale that
+// keeps them within fp16's range.  Such a scale holds for a whole block, in
+// which numbers differ widely (a state of 10^6 times the values, decays to
+// e^-30); with lo scaled up they keep all 22 bits down to 2^-26 of the largest,
+// and what lies below 2^-48 of it counts as zero.  (With lo as it is the error
+// begins at 2^-15: a state of 10^6 times the values, decayed by e^-0.5 a token,
+// ended 10^-3 off.)  Each row of keys and queries is scaled by a power of two of
+// its own (the row's norm is applied afterwards): fp16 and bf16 rows are then
+// exact in fp16 but for elements below 2^-26 of the row's largest, which are off
+// by 2^-37 of it at most.
 // An operand pair costs two products against an exact operand and three
 // against another pair; fp32 matrix instructions take 8 times as long as
 // fp16's for the same product.
@@ -194,10 +201,13 @@ __device__ __forceinline__ Pow2 pow2_scale(float m) {
   const int f = min(266 - static_cast<int>((__float_as_uint(m) >> 23) & 255u), 253);
   return {__uint_as_float(static_cast<uint32_t>(f) << 23), __uint_as_float(static_cast<uint32_t>(254 - f) << 23)};
 }
-// fp16 pair of v: hi = nearest fp16, lo = nearest fp16 of the exact rest
+// fp16 pair of v = hi + lo / 2^11: hi = nearest fp16, lo from the exact rest.
+// With lo scaled up the pair keeps 22 bits of all v above 2^-14, where the
+// scaled operands reach 2^13, and is off by 2^-36 at most below.
+constexpr float kLoUp = 0x1p11f, kLoDown = 0x1p-11f;
 __device__ __forceinline__ void split16(float v, _Float16& hi, _Float16& lo) {
   hi = static_cast<_Float16>(v);
-  lo = static_cast<_Float16>(v - static_cast<float>(hi));
+  lo = static_cast<_Float16>((v - static_cast<float>(hi)) * kLoUp);
 }
 // max and sum over the four lanes that share a column (lane % 16): swaps of
 // rows of 16 lanes and of halves
@@ -476,12 +486,12 @@ __global__ __launch_bounds__(256, 4) void k_gdn_blocks(GdnArgs a, uint8_t* __res
       // beta in [0, 2]) and rk <= 2^-12 (rows are scaled to a largest value of
       // 2^12 or more).
       const float gmax = wave_max(eg), bmax = wave_max(bt), dd = bmax * 0x1p-12f;
-      const float sb = wave_sum(bt), sg = wave_sum(bt * left), gamma = exp2_of(last);
+      const float sg = wave_sum(bt * left), gamma = exp2_of(last);
       if (lane == 0) {
         vec[kScGamma] = gamma;
         vec[kScGmax] = gmax;
-        vec[kScD0] = dd * (1.0f + sb);
-        vec[kScD1] = dd * gmax;
+        vec[kScD0] = dd * (1.0f + sg);
+        vec[kScD1] = dd * gamma;
         vec[kScS0] = sg;
       }
     }
@@ -792,7 +802,7 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
     {
       const float vm = fmaxf(fmaxf(vmax[0][n], vmax[1][n]), fmaxf(vmax[2][n], vmax[3][n]));
       const Pow2 pr = pow2_scale(fmaf(gmax, bound, vm)), pd = pow2_scale(fmaf(cd1, bound, cd0 * vm));
-      fd = inv_t * pr.down * pd.up;
+      fd = inv_t * pd.up * pr.down;   // in this order: nothing on the way leaves fp32's range
       fo = inv_m * pr.down;
       inv_d = pd.down;
       bound = cs0 * vm;   // the next block's, completed below
@@ -826,7 +836,7 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         _Float16 vh, vl;
-        split16(fmaf(-as[r], X[0][r] + X[1][r], vs[r]), vh, vl);
+        split16(fmaf(-as[r], fmaf(kLoDown, X[1][r], X[0][r]), vs[r]), vh, vl);
         rh[r] = vh;
         rl[r] = vl;
       }
@@ -844,27 +854,29 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
         rl[s] = *reinterpret_cast<const f16x8*>(&rf[s][1][lane][0]);
       }
     }
-    f32x4 Y = {0, 0, 0, 0};
+    f32x4 Y = {0, 0, 0, 0}, Y1 = {0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       Y = mfma(as_frag(qf[s]), sh[s], Y);
-      Y = mfma(as_frag(qf[s]), sl[s], Y);
+      Y1 = mfma(as_frag(qf[s]), sl[s], Y1);
     }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) Y[r] = fmaf(kLoDown, Y1[r], Y[r]);
     {
       f32x4 D0 = {0, 0, 0, 0}, D1 = {0, 0, 0, 0};
-      D0 = mfma(as_frag(th[0]), rh[0], D0);
       D1 = mfma(as_frag(tl[0]), rh[0], D1);
-      D0 = mfma(as_frag(th[0]), rl[0], D0);
+      D0 = mfma(as_frag(th[0]), rh[0], D0);
+      D1 = mfma(as_frag(th[0]), rl[0], D1);
       if (w >= 2) {
-        D1 = mfma(as_frag(tl[1]), rh[1], D1);
         D0 = mfma(as_frag(th[1]), rh[1], D0);
+        D1 = mfma(as_frag(tl[1]), rh[1], D1);
         D1 = mfma(as_frag(th[1]), rl[1], D1);
       }
       f16x4 dh, dl;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         _Float16 vh, vl;
-        split16((D0[r] + D1[r]) * fd, vh, vl);
+        split16(fmaf(kLoDown, D1[r], D0[r]) * fd, vh, vl);
         dh[r] = vh;
         dl[r] = vl;
       }
@@ -884,32 +896,32 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
       dh[s] = *reinterpret_cast<const f16x8*>(&df[s][0][lane][0]);
       dl[s] = *reinterpret_cast<const f16x8*>(&df[s][1][lane][0]);
     }
-    f32x4 O = mfma(as_frag(ml[0]), rh[0], f32x4{0, 0, 0, 0});
-    O = mfma(as_frag(mh[0]), rl[0], O);
-    O = mfma(as_frag(mh[0]), rh[0], O);
+    f32x4 O1 = mfma(as_frag(ml[0]), rh[0], f32x4{0, 0, 0, 0}), O = mfma(as_frag(mh[0]), rh[0], f32x4{0, 0, 0, 0});
+    O1 = mfma(as_frag(mh[0]), rl[0], O1);
     if (w >= 2) {
-      O = mfma(as_frag(ml[1]), rh[1], O);
-      O = mfma(as_frag(mh[1]), rl[1], O);
+      O1 = mfma(as_frag(ml[1]), rh[1], O1);
       O = mfma(as_frag(mh[1]), rh[1], O);
+      O1 = mfma(as_frag(mh[1]), rl[1], O1);
     }
-    f32x4 u[2];
+    f32x4 u[2], u1[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       u[m] = mfma(as_frag(kt[2 * m]), dh[0], f32x4{0, 0, 0, 0});
-      u[m] = mfma(as_frag(kt[2 * m]), dl[0], u[m]);
+      u1[m] = mfma(as_frag(kt[2 * m]), dl[0], f32x4{0, 0, 0, 0});
       u[m] = mfma(as_frag(kt[2 * m + 1]), dh[1], u[m]);
-      u[m] = mfma(as_frag(kt[2 * m + 1]), dl[1], u[m]);
+      u1[m] = mfma(as_frag(kt[2 * m + 1]), dl[1], u1[m]);
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) S[m][r] = fmaf(inv_d, u[m][r], gamma * S[m][r]);
+      for (int r = 0; r < 4; ++r)
+        S[m][r] = fmaf(inv_d, fmaf(kLoDown, u1[m][r], u[m][r]), gamma * S[m][r]);
     const float et[4] = {ev.x, ev.y, ev.z, ev.w}, rt[4] = {rv.x, rv.y, rv.z, rv.w};
     float* op = obase + static_cast<size_t>(c) * kBlock * row_el;
     const int left = t1 - (t0 + c * kBlock + 16 * w);   // uniform
     float v[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = rt[r] * fmaf(et[r] * inv_s, Y[r], fo * O[r]);
+    for (int r = 0; r < 4; ++r) v[r] = rt[r] * fmaf(et[r] * inv_s, Y[r], fo * fmaf(kLoDown, O1[r], O[r]));
     if (left >= 16) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) *(op + r * row_el + el) = v[r];

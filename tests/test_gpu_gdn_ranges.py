@@ -186,3 +186,60 @@ def test_captured_with_rises_that_come_and_go():
         run(1)
         torch.cuda.synchronize()
         assert torch.equal(o[0], o[1]) and torch.equal(s[0], s[1])
+
+
+def uneven(edit, d, lens):
+    """Gives the inputs numbers of very different size within a block."""
+    import torch
+    n = sum(lens)
+    gen = torch.Generator().manual_seed(5)
+    kind, _, arg = edit.partition(" ")
+    if kind == "jump":   # a state far above the values after it
+        d["g"][:] = -0.2
+        d["g"][n // 2] = 20.0
+    elif kind == "large":
+        d["g"][:] = -float(arg)
+        d["state"] *= 1e6
+    elif kind == "novalues":
+        d["g"][:] = -float(arg)
+        d["v"].zero_()
+    elif kind == "values":   # of 10^-5 to 10^5 times their size, by token
+        d["v"] = (d["v"].float() * 10 ** (10 * torch.rand(n, 1, 1, generator=gen) - 5)).to(d["v"].dtype)
+    elif kind == "betas":
+        d["beta"] *= 10 ** (-8 * torch.rand(d["beta"].shape, generator=gen))
+    elif kind == "tail":
+        d["g"][:] = -0.5
+        d["v"][n // 2:] *= 1e-6
+    elif kind == "all":
+        d["v"] *= float(arg)
+        d["state"] *= float(arg)
+    else:   # tokens that only decay
+        assert kind == "pads"
+        d["g"][:] = -5.0
+        for e in range(54, n, 32):
+            d["v"][e - 10:e] = 0
+            d["beta"][e - 10:e] = 0
+
+
+@pytest.mark.parametrize("lens", LENS + [[70, 3, 129, 64]], ids=IDS + ["batch"])
+@pytest.mark.parametrize("edit", ["jump", "large 0.2", "large 0.5", "large 2", "novalues 0.05", "novalues 0.2", "values",
+                                  "betas", "tail", "all 1e-34"])
+def test_numbers_of_very_different_size_in_a_block(lens, edit):
+    d = inputs(lens, 2, 4, 48, "bf16", 37)
+    uneven(edit, d, lens)
+    hold(d, lens, "bf16")
+
+
+@pytest.mark.parametrize("edit", ["novalues 0.5", "novalues 2", "pads"])
+def test_what_a_block_shrinks_beyond_its_digits(edit):
+    # An operand below 2^-48 of the block's largest counts as zero.  At most 64
+    # tokens' products of two such operands, and 64 of one with a key, meet in a
+    # result: 2^-40 of the state before the block and of its values on top
+    lens = [150]
+    d = inputs(lens, 2, 4, 48, "bf16", 37)
+    uneven(edit, d, lens)
+    got_o, got_s = (x.astype(np.float64) for x in gpu(d, lens, "bf16"))
+    o, S, bo, bs = oracle_with_bounds(d, lens)
+    size = np.linalg.norm(d["state"].double().numpy()) + np.linalg.norm(d["v"].double().numpy(), axis=-1).max()
+    assert (np.linalg.norm(got_o - o, axis=-1) <= bo + 2.0 ** -40 * Q_SCALE * size).all()
+    assert (np.sqrt(((got_s - S) ** 2).sum((-1, -2))) <= bs + 2.0 ** -40 * size).all()
