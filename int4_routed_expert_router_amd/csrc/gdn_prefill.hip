@@ -71,18 +71,26 @@ __device__ __forceinline__ void run_tokens(const GdnArgs& a, int b, int h, int t
     for (int z = 0; z < NS; ++z) vt[z] = act_to_f32<ACT>(vv[z]);
     load(min(t + 1, t1 - 1));
     float qn[8], kn[8], qq = 0, kk = 0, kq = 0;
+    // the rows are normalised before they meet each other or the state: a raw
+    // product may overflow where the normalised one is finite (or, with a row
+    // whose squares overflow, 0)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       qn[j] = act_to_f32<ACT>((qw[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
       kn[j] = act_to_f32<ACT>((kw[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
       qq = fmaf(qn[j], qn[j], qq);
       kk = fmaf(kn[j], kn[j], kk);
-      kq = fmaf(kn[j], qn[j], kq);
     }
     qq = row_sum16(qq);
     kk = row_sum16(kk);
-    kq = row_sum16(kq);
     const float rq = a.q_scale * __builtin_amdgcn_rsqf(qq + kEps), rk = __builtin_amdgcn_rsqf(kk + kEps);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      qn[j] *= rq;
+      kn[j] *= rk;
+      kq = fmaf(kn[j], qn[j], kq);
+    }
+    kq = row_sum16(kq);
     float* o = a.o + (static_cast<size_t>(t) * a.Hv + h) * a.dv;
 #pragma unroll
     for (int z = 0; z < NS; ++z) {
@@ -94,10 +102,10 @@ __device__ __forceinline__ void run_tokens(const GdnArgs& a, int b, int h, int t
       }
       u = row_sum16(u);
       w = row_sum16(w);
-      const float d = bt * fmaf(-alpha, u * rk, vt[z]), dk = d * rk;
+      const float d = bt * fmaf(-alpha, u, vt[z]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[z][j] = fmaf(dk, kn[j], alpha * s[z][j]);
-      if (c0 == 0 && (NS == 1 || row0 + 16 * z < a.dv)) o[row[z]] = fmaf(dk * rq, kq, alpha * (w * rq));
+      for (int j = 0; j < 8; ++j) s[z][j] = fmaf(d, kn[j], alpha * s[z][j]);
+      if (c0 == 0 && (NS == 1 || row0 + 16 * z < a.dv)) o[row[z]] = fmaf(d, kq, alpha * w);
     }
   }
 #pragma unroll

@@ -243,3 +243,25 @@ def test_what_a_block_shrinks_beyond_its_digits(edit):
     size = np.linalg.norm(d["state"].double().numpy()) + np.linalg.norm(d["v"].double().numpy(), axis=-1).max()
     assert (np.linalg.norm(got_o - o, axis=-1) <= bo + 2.0 ** -40 * Q_SCALE * size).all()
     assert (np.sqrt(((got_s - S) ** 2).sum((-1, -2))) <= bs + 2.0 ** -40 * size).all()
+
+
+@pytest.mark.parametrize("lens", [[9], [24], [90]], ids=["short", "longest short", "blocks"])
+def test_overflowing_rows_of_both_kinds_and_large_states(lens):
+    # a row whose sum of squares overflows counts as zero, also where the other
+    # row of its token, or the state, is large; finite rows up to that size are
+    # normalised before they meet a large state
+    d = inputs(lens, 1, 2, 32, "bf16", 31)
+    d["state"] *= 100.0
+    d["state"][:, 1] *= 1e25
+    d["k"][5], d["q"][5] = 1e15, -1e15   # not overflowing
+    d["k"][6, 0, ::2] = 3e18
+    zero = {k: v.clone() for k, v in d.items()}
+    for t, k, q in ((1, 1e25, 1e25), (2, 3e38, 10.0), (3, 10.0, 3e38), (7, -3e38, 3e38)):
+        for key, x in (("k", k), ("q", q)):
+            d[key][t] = zero[key][t] = x
+            if abs(x) > 1e19:
+                zero[key][t] = 0
+    zero["k"][6] = 0   # 64 x 9e36 is above fp32's largest number
+    d["k"][8, 0, 0] = zero["k"][8, 0, 0] = 3e38   # one element alone
+    zero["k"][8] = 0
+    hold(d, lens, "bf16", want=zero)
