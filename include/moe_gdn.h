@@ -63,7 +63,8 @@ moe_status moe_gdn_step(const moe_gdn_desc* desc, const void* q, const void* k, 
  * end before its start as an empty sequence; results of overlapping sequences
  * are not defined.
  *
- * desc->batch is B; q, k 16-byte aligned; n_tokens up to 2^30.  The workspace
+ * desc->batch is B; q, k 16-byte aligned; n_tokens up to 2^30 and
+ * n_tokens / 64 + B below 2^24.  The workspace
  * (256-byte aligned, moe_gdn_prefill_workspace_bytes) is only used while the
  * call runs.  State and sums are fp32; the results are those of the tokens
  * taken one by one up to fp32 rounding (in a block of 64 tokens, see below, also

@@ -189,6 +189,8 @@ constexpr size_t kKeyBytes = 48 * 1024;
 constexpr size_t kHeadBytes = 25 * 1024;
 constexpr int kScGamma = 192, kScInvT = 193, kScInvM = 194, kScGmax = 195, kScD0 = 196, kScD1 = 197, kScS0 = 198;
 
+constexpr size_t kMaxSlots = (1 << 24) - 1;   // a grid dimension holds fewer than 2^32 threads, 256 per slot
+
 __host__ __device__ inline size_t prefill_slots(int B, int N) { return static_cast<size_t>(N) / kBlock + B; }
 
 // offset of the value heads' part, behind the key heads'
@@ -642,7 +644,7 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
   // a sequence's workgroups are dealt to the eight dies in runs, so that the
   // workgroups that read one key head's operands share an L2
   const int slices = a.dv / 16, units = a.Hv * slices, run = (units + 7) / 8;
-  const int b = blockIdx.x / (8 * run), i = blockIdx.x % (8 * run);
+  const int b = blockIdx.y, i = blockIdx.x;
   const int unit = (i % 8) * run + i / 8;
   if (unit >= units) return;
   const int h = unit / slices, dv0 = (unit % slices) * 16;
@@ -996,7 +998,7 @@ hipError_t launch_prefill(const GdnArgs& a, uint8_t* ws, hipStream_t s) {
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int units = a.Hv * (a.dv / 16), run = (units + 7) / 8;
-  hipLaunchKernelGGL(k_gdn_scan<ACT>, dim3(static_cast<uint32_t>(a.B) * 8 * run), dim3(256), 0, s, a, ws);
+  hipLaunchKernelGGL(k_gdn_scan<ACT>, dim3(8 * run, a.B), dim3(256), 0, s, a, ws);
   return hipGetLastError();
 }
 
@@ -1011,6 +1013,8 @@ moe_status check_prefill(const moe_gdn_desc* d, int32_t N) {
   if (d->act_dtype != MOE_F16 && d->act_dtype != MOE_BF16)
     return set_error(MOE_EINVAL, "act_dtype=%d is not MOE_F16/MOE_BF16", d->act_dtype);
   if (N < 0 || N > (1 << 30)) return set_error(MOE_ESHAPE, "n_tokens=%d must be in [0, 2^30]", N);
+  if (prefill_slots(d->batch, N) > kMaxSlots)
+    return set_error(MOE_ESHAPE, "n_tokens=%d / 64 + batch=%d must be below 2^24", N, d->batch);
   return MOE_OK;
 }
 
