@@ -658,20 +658,10 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
   const uint8_t* kp = ws + (static_cast<size_t>(slot0) * a.Hk + hk) * kKeyBytes;
   const uint8_t* hp = ws + prefill_ws_heads(a) + (static_cast<size_t>(slot0) * a.Hv + h) * kHeadBytes;
   const size_t kstep = a.Hk * kKeyBytes, hstep = a.Hv * kHeadBytes;
-  // blocks before the first that goes token by token, 64 at a time (a test in
-  // the blocks' loop makes it longer: 8192 tokens 358 us instead of 313)
-  int end = t1 - t0 <= kShort ? 0 : nblk;
-  for (int c = 0; c < end; c += 64) {
-    const size_t i = min(c + lane, nblk - 1);
-    const unsigned long long m =
-        __ballot(*reinterpret_cast<const float*>(hp + i * hstep + 24 * 1024 + 4 * kScGamma) < 0.0f);
-    if (m != 0) end = min(c + __ffsll(m) - 1, nblk);
-  }
-  end = __builtin_amdgcn_readfirstlane(end);
-  if (end == 0) {
-    run_tokens<ACT, 1>(a, b, h, t0, t1, dv0 + (tid >> 4));
-    return;
-  }
+  auto mark = [&](int c) {   // of block c, below 0 where it goes token by token
+    return *reinterpret_cast<const float*>(hp + static_cast<size_t>(min(c, nblk - 1)) * hstep + 24 * 1024 + 4 * kScGamma);
+  };
+  const float first_marks = mark(lane);
   // uniform bases and 32-bit lane offsets: rows 16w + 4q + r of a block
   const uint32_t row_el = static_cast<uint32_t>(a.Hv) * a.dv;
   const uint16_t* vbase = a.v + (static_cast<size_t>(t0 + 16 * w) * a.Hv + h) * a.dv;
@@ -767,6 +757,18 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
   load_cols(kp);
   load_values(1, vb);
 
+  // blocks before the first that goes token by token, 64 at a time (a test in
+  // the blocks' loop makes it longer: 8192 tokens 358 us instead of 313)
+  int end = t1 - t0 <= kShort ? 0 : nblk;
+  for (int c = 0; c < end; c += 64) {
+    const unsigned long long m = __ballot((c == 0 ? first_marks : mark(c + lane)) < 0.0f);
+    if (m != 0) end = min(c + __ffsll(m) - 1, nblk);
+  }
+  end = __builtin_amdgcn_readfirstlane(end);
+  if (end == 0) {
+    run_tokens<ACT, 1>(a, b, h, t0, t1, dv0 + (tid >> 4));
+    return;
+  }
   // the largest values of the state rows
   {
     float m = 0.0f;
