@@ -53,7 +53,7 @@ typedef struct {
 
 /* Choice from given logits.  logits: device fp32, row t at logits + t *
  * logits_stride (elements; >= E, >= E + 1 with shared_gate), as moe_route
- * writes them with logits_stride E + 1.  bias: device fp32 [E] or NULL.
+ * writes them with logits_stride E + 1.  n_tokens up to 2^26 - 4.  bias: device fp32 [E] or NULL.
  * Outputs (device): topk_idx [T][K] int32, topk_w [T][K] fp32,
  * shared_gate_or_null [T] fp32 = sigmoid of column E of the logits. */
 moe_status moe_select(const moe_select_desc* desc, const float* logits, int64_t logits_stride,
@@ -62,8 +62,8 @@ moe_status moe_select(const moe_select_desc* desc, const float* logits, int64_t 
 
 /* moe_route with this choice: router GEMV (logits without bias), then the
  * choice above with router_bias as the balance bias.  sel must agree with
- * desc in n_experts and top_k.  Workspace and the other arguments as in
- * moe_route. */
+ * desc in n_experts and top_k.  n_tokens as in moe_select, workspace and the
+ * other arguments as in moe_route. */
 moe_status moe_route_scored(const moe_layer_desc* desc, const moe_select_desc* sel, const moe_layer_weights* w,
                             const void* x, int32_t n_tokens, int32_t* topk_idx, float* topk_w, float* shared_gate,
                             float* logits_or_null, void* ws, size_t ws_bytes, moe_stream stream);

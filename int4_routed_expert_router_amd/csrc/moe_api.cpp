@@ -472,7 +472,8 @@ moe_status moe_route_scored(const moe_layer_desc* d, const moe_select_desc* sel,
     return fail(MOE_ESHAPE, "the select desc (%d of %d experts) differs from the layer's (%d of %d)", sel->top_k,
                 sel->n_experts, d->top_k, d->n_experts);
   if ((st = check_weights(d, w))) return st;
-  if (T < 0) return fail(MOE_ESHAPE, "n_tokens=%d < 0", T);
+  if (T < 0 || T > moe::kMaxSelectTokens)
+    return fail(MOE_ESHAPE, "n_tokens=%d must be in [0, %d]", T, moe::kMaxSelectTokens);
   if (T == 0) return ok();
   if (!x || !aligned(x, 16)) return fail(MOE_EINVAL, "x must be a 16-byte aligned device pointer");
   if (!topk_idx || !topk_w) return fail(MOE_EINVAL, "topk_idx and topk_w are required");

@@ -134,6 +134,9 @@ struct SelectArgs {
   int n_part, T, E, K, score, n_group, top_groups, group_top, renorm;
   float scale;
 };
+// Most tokens of one call: a workgroup of 256 threads takes four, and a grid
+// holds fewer than 2^32 threads.
+constexpr int kMaxSelectTokens = 4 * ((1 << 24) - 1);
 hipError_t launch_select(const SelectArgs& a, hipStream_t s);
 hipError_t launch_permute(const int32_t* idx, int n, int E, int32_t* off, int32_t* perm, int32_t* inv,
                           const UnitPlan* plan, hipStream_t s);

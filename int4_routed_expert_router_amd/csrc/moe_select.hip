@@ -417,7 +417,8 @@ extern "C" moe_status moe_select(const moe_select_desc* d, const float* logits, 
   moe::SelectArgs a;
   const moe_status st = moe::check_select(d, &a);
   if (st) return st;
-  if (T < 0) return set_error(MOE_ESHAPE, "n_tokens=%d < 0", T);
+  if (T < 0 || T > moe::kMaxSelectTokens)
+    return set_error(MOE_ESHAPE, "n_tokens=%d must be in [0, %d]", T, moe::kMaxSelectTokens);
   const int64_t need = shared_gate ? a.E + 1 : a.E;
   if (stride < need) return set_error(MOE_ESHAPE, "logits_stride=%lld < %lld", (long long)stride, (long long)need);
   if (T == 0) return set_error(MOE_OK, "");
