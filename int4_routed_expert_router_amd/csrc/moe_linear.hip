@@ -188,11 +188,14 @@ __global__ __launch_bounds__(512, 2) void k_linear_tile(const uint8_t* __restric
   __shared__ float sums[2][2][kTileT][5];         // [half][4 units' buffer][token][unit], padded
   const int tid = threadIdx.x & 255, lane = tid & 63, n = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = wave >> 2;
-  // the token tiles of one row tile run on the same die, one after the other
-  const int nt = (T + kTileT - 1) / kTileT, id = blockIdx.x / 8;
-  const int r0 = ((id / nt) * 8 + blockIdx.x % 8) * (kTileN / 32), tok0 = (id % nt) * kTileT;
+  // The tiles, a row tile's token tiles one after the other, are dealt to the
+  // eight dies in runs: each die has the same number of them, and a row tile's
+  // lie on one die or a few (16384 tokens, 64 outputs 27 us; with row tile r on
+  // die r mod 8 107, and 1152 outputs 137 against 210).
+  const int nt = (T + kTileT - 1) / kTileT, tile = (blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8;
+  const int r0 = tile / nt * (kTileN / 32), tok0 = tile % nt * kTileT;
   const int np = (N + 31) / 32, nc = K / 64, ng = K / G;
-  if (r0 >= np) return;   // the grid is a multiple of 8 row tiles
+  if (r0 >= np) return;   // the grid is a multiple of 8 tiles
   const int p = r0 + (wave & 3);
   const int pc = min(p, np - 1);   // a wave without rows still stages
   const int nit = (nc + 1) / 2, mine = (nc + 1 - half) / 2;   // steps, and this half's chunks
@@ -401,13 +404,13 @@ hipError_t launch_linear(const moe_linear_desc* d, const uint8_t* packed, const 
   // The 128 x 128 tiles where there are enough of them to fill the chip half,
   // k_linear otherwise (us, tiles against k_linear; 2048 inputs): 64 tiles
   // 26.6 / 18.8 (512 tokens, 2048 outputs) and 26.4 / 18.6 (128 tokens, 8192);
-  // 128 tiles 27.4 / 34.6, 27.5 / 34.5 and 30.3 / 35.4 (4096 tokens, 512
+  // 128 tiles 27.4 / 34.6, 27.5 / 34.5 and 27.4 / 35.4 (4096 tokens, 512
   // outputs).  Up to 64 tokens half of a tile's tokens are padding, which only
   // pays when k_linear is bound by arithmetic: 64 tokens 26 / 19 with 128
   // tiles, 51 / 67 with 512, 125 / 154 with 1187; 48 tokens 51 / 56 and 124 /
   // 127; 32 tokens 50 / 35 and 123 / 78.
   if (T > 48 && static_cast<int64_t>(nt) * nr >= (T > 64 ? 128 : 512)) {
-    const dim3 grid((nr + 7) / 8 * 8 * nt), block(512);
+    const dim3 grid((nr * nt + 7) / 8 * 8), block(512);
     if (G == 32) hipLaunchKernelGGL((k_linear_tile<ACT, RES, true>), grid, block, 0, s, packed, x, y, T, N, K, G, off);
     else hipLaunchKernelGGL((k_linear_tile<ACT, RES, false>), grid, block, 0, s, packed, x, y, T, N, K, G, off);
     return hipGetLastError();

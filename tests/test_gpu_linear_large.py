@@ -25,3 +25,22 @@ def test_more_packed_words_than_one_grid_dimension(K, N, G):
     for t, k in enumerate(at):
         q = (words[:, k // 8] >> (4 * (k % 8))) & 15
         assert torch.equal(y[t], q * s[:, k // G].float() + b[:, k // G].float())
+
+
+@pytest.mark.parametrize("T,N,G", [(16500, 40, 64), (128 * 128, 128, 32), (9001, 300, 128), (4999, 1157, 64),
+                                   (700, 3001, 64), (130, 16385, 32)])
+def test_tiles_of_any_count(T, N, G):
+    # few and uneven row and token tiles; small whole numbers, exact in fp32
+    import torch
+    from int4_routed_expert_router_amd import api
+    K = 128
+    g = torch.Generator(device="cuda").manual_seed(T + N)
+    words = torch.randint(-2 ** 31, 2 ** 31, (N, K // 8), generator=g, device="cuda").to(torch.int32)
+    s = torch.randint(1, 4, (N, K // G), generator=g, device="cuda").half()
+    b = torch.randint(-20, 4, (N, K // G), generator=g, device="cuda").half()
+    x = torch.randint(-2, 3, (T, K), generator=g, device="cuda").bfloat16()
+    y = torch.full((T + 3, N), 7.0, device="cuda")
+    api.linear(api.Linear(K, N, G, words, s, b), x, y[:T])
+    q = torch.stack([(words >> (4 * j)) & 15 for j in range(8)], -1).view(N, K)
+    w = q * s.double().repeat_interleave(G, 1) + b.double().repeat_interleave(G, 1)
+    assert torch.equal(y[:T].double(), x.double() @ w.t().contiguous()) and (y[T:] == 7.0).all()
