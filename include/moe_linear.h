@@ -53,7 +53,8 @@ moe_status moe_linear_pack(int32_t in_dim, int32_t out_dim, int32_t group_size, 
                            const uint16_t* scale, const uint16_t* bias, uint8_t* packed, moe_stream stream);
 
 /* y [T][N] (out_dtype, rows back to back) of x [T][K] (16-byte aligned) and
- * the packed weights.  n_tokens up to 2^20. */
+ * the packed weights.  n_tokens up to 2^20, and ceil(n_tokens / 128) *
+ * ceil(N / 128) up to 2^23 - 8. */
 moe_status moe_linear_forward(const moe_linear_desc* desc, const uint8_t* packed, const void* x, int32_t n_tokens,
                               void* y, moe_stream stream);
 

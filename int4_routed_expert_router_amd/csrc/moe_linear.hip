@@ -388,6 +388,7 @@ __global__ __launch_bounds__(256) void k_linear_pack(const uint32_t* __restrict_
 }
 
 constexpr int kLinMaxIn = 65536, kLinMaxOut = 1 << 20, kLinMaxTokens = 1 << 20;
+constexpr int kLinMaxTiles = (1 << 23) - 8;   // a grid holds fewer than 2^32 threads, 512 per tile
 
 bool linear_shape_ok(int K, int N, int G) {
   return K >= 64 && K <= kLinMaxIn && K % 64 == 0 && N >= 1 && N <= kLinMaxOut &&
@@ -481,6 +482,9 @@ extern "C" moe_status moe_linear_forward(const moe_linear_desc* d, const uint8_t
   if (d->out_dtype != MOE_F16 && d->out_dtype != MOE_BF16 && d->out_dtype != MOE_F32)
     return set_error(MOE_EINVAL, "out_dtype=%d is not MOE_F16/MOE_BF16/MOE_F32", d->out_dtype);
   if (T < 0 || T > moe::kLinMaxTokens) return set_error(MOE_ESHAPE, "n_tokens=%d must be in [0, %d]", T, moe::kLinMaxTokens);
+  if (static_cast<int64_t>((T + moe::kTileT - 1) / moe::kTileT) * ((d->out_dim + moe::kTileN - 1) / moe::kTileN) >
+      moe::kLinMaxTiles)
+    return set_error(MOE_ESHAPE, "n_tokens=%d x out_dim=%d is more than 2^23 - 8 tiles of 128 x 128", T, d->out_dim);
   if (T == 0) return set_error(MOE_OK, "");
   if (!packed || !moe::lin_aligned(packed, 256))
     return set_error(MOE_EINVAL, "packed must be a 256-byte aligned device pointer");
