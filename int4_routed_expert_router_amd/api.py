@@ -7,6 +7,7 @@ asynchronously on the current torch stream unless a stream is given.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import dataclasses
 
@@ -63,16 +64,21 @@ def _stream(stream):
 
 
 def _scratch(desc, T, device, stream):
-    """A temporary workspace for one call.  It is allocated on the current
-    stream; when the call runs on another torch stream the tensor is recorded
-    on that stream too, so the caching allocator does not hand its memory out
-    again before the call's kernels have finished with it."""
-    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+    """A temporary workspace for one call."""
+    with _allocating_on(stream):
+        return workspace(desc, T, device)
+
+
+def _allocating_on(stream):
+    """Context in which a call's temporary memory is allocated: that of the
+    stream it runs on.  The caching allocator hands out a stream's freed blocks
+    again in that stream's order only, so memory of another stream's might
+    still be in use by work that waits there."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
         raise ValueError("pass ws explicitly when stream is a raw stream handle")
-    ws = workspace(desc, T, device)
-    if stream is not None and stream != torch.cuda.current_stream(ws.device):
-        ws.record_stream(stream)
-    return ws
+    return torch.cuda.stream(stream)
 
 
 def _arg(t, name, dtypes, numel, dev):
@@ -545,11 +551,8 @@ def gdn_prefill(q, k, v, g, beta, state, o, seq_off, q_scale, act_dtype="bf16", 
             _arg(state, "state", _F32, B * Hv * dv * dk, dev), _arg(o, "o", _F32, N * Hv * dv, dev))
     d = GdnDesc(B, Hk, Hv, dk, dv, _ACT.get(act_dtype, 0))
     if ws is None:
-        if stream is not None and not isinstance(stream, torch.cuda.Stream):
-            raise ValueError("pass ws explicitly when stream is a raw stream handle")
-        ws = gdn_prefill_workspace(B, N, Hk, Hv, dv, act_dtype, dk, q.device)
-        if stream is not None and stream != torch.cuda.current_stream(ws.device):
-            ws.record_stream(stream)
+        with _allocating_on(stream):
+            ws = gdn_prefill_workspace(B, N, Hk, Hv, dv, act_dtype, dk, q.device)
     _call_on(dev, lib().moe_gdn_prefill, C.byref(d), *args, _arg(ws, "ws", (torch.uint8,), None, dev), ws.numel(),
              _stream_on(dev, stream))
 
@@ -564,7 +567,10 @@ class Linear:
     words: [out, in/8] int32, value 8i + j of a row in bits 4j..4j+3 of its
     word i; scale, bias: [out, in/group] float16 (or int16 bits); act_dtype:
     dtype of the activations, "f16" | "bf16".  The source tensors may be
-    freed once the pack call's stream has passed it."""
+    freed once the pack call's stream has passed it.  A linear that was packed
+    on one stream is used on another after the caller has ordered the two; the
+    memory belongs to the packing stream, and other streams than that and the
+    one current here are recorded on .packed by the caller before it is freed."""
 
     def __init__(self, in_dim, out_dim, group_size, words, scale, bias, act_dtype="bf16", stream=None):
         n = int(lib().moe_linear_bytes(in_dim, out_dim, group_size))
@@ -578,13 +584,17 @@ class Linear:
         args = (_arg(words, "words", _I32, out_dim * in_dim // 8, dev), _arg(scale, "scale", f16, ng, dev),
                 _arg(bias, "bias", f16, ng, dev))
         self.in_dim, self.out_dim, self.group_size, self.act_dtype = in_dim, out_dim, group_size, act_dtype
-        self.packed = torch.empty(n, dtype=torch.uint8, device=words.device)
+        # memory of the packing stream (see _allocating_on), which the current
+        # stream may use as well: freed blocks wait for both
+        side = torch.cuda.ExternalStream(stream, words.device) if isinstance(stream, int) else stream
+        with _allocating_on(side):
+            self.packed = torch.empty(n, dtype=torch.uint8, device=words.device)
+        if side is not None:
+            self.packed.record_stream(torch.cuda.current_stream(words.device))
         self._acts = _ACTS[act_dtype]
         self._c = {t: LinearDesc(in_dim, out_dim, group_size, _ACT[act_dtype], o) for t, o in _OUT.items()}
         _call_on(dev, lib().moe_linear_pack, in_dim, out_dim, group_size, *args, self.packed.data_ptr(),
                  _stream_on(dev, stream))
-        if isinstance(stream, torch.cuda.Stream):
-            self.packed.record_stream(stream)
 
 
 def linear(lin, x, y, stream=None):
