@@ -167,6 +167,9 @@ __global__ __launch_bounds__(64 * kLinWaves) void k_linear(const uint8_t* __rest
 // which costs a quarter of the main products' matrix time and spares 64
 // multiply-adds a chunk.
 //
+// With groups of 32 twice the scales and multiply-adds do not fit: 256 registers
+// and 36 spilled, 47 us against 29 (499 tokens, 2048 inputs, 8192 outputs).
+//
 // 499 tokens, 2048 inputs, 8192 outputs: 32 us, 525 TF/s.  Bound by one
 // workgroup's chain per compute unit: conversions, products and scalings of a
 // chunk add up where its two waves per SIMD do not overlap; with four waves (one
@@ -402,15 +405,22 @@ hipError_t launch_linear(const moe_linear_desc* d, const uint8_t* packed, const 
   const int K = d->in_dim, N = d->out_dim, G = d->group_size;
   const uint64_t off = padded_rows(N) * K / 2;
   const int np = (N + 31) / 32, nt = (T + kTileT - 1) / kTileT, nr = (N + kTileN - 1) / kTileN;
-  // The 128 x 128 tiles where there are enough of them to fill the chip half,
-  // k_linear otherwise (us, tiles against k_linear; 2048 inputs): 64 tiles
-  // 26.6 / 18.8 (512 tokens, 2048 outputs) and 26.4 / 18.6 (128 tokens, 8192);
-  // 128 tiles 27.4 / 34.6, 27.5 / 34.5 and 27.4 / 35.4 (4096 tokens, 512
-  // outputs).  Up to 64 tokens half of a tile's tokens are padding, which only
-  // pays when k_linear is bound by arithmetic: 64 tokens 26 / 19 with 128
-  // tiles, 51 / 67 with 512, 125 / 154 with 1187; 48 tokens 51 / 56 and 124 /
-  // 127; 32 tokens 50 / 35 and 123 / 78.
-  if (T > 48 && static_cast<int64_t>(nt) * nr >= (T > 64 ? 128 : 512)) {
+  // A round of up to 256 tiles (one per compute unit, full or not) takes as long
+  // as some 1600 workgroups of k_linear (2560 with groups of 32, where the tile
+  // kernel spills), and the kernel that needs less is taken.  us, tiles against
+  // k_linear, 2048 inputs:
+  //   128 tokens, 8192 outputs (1024 workgroups, 1 round)   26.5 / 18.8, groups of 32 43.8 / 21.3
+  //   128 tokens, 12603 outputs (1576, 1)                   26.6 / 31.2
+  //   128 tokens, 16384 outputs (2048, 1)                   27.0 / 34.7, groups of 32 44.7 / 37.6
+  //   384 tokens, 6684 outputs (2508, 1)                    groups of 32 44.5 / 46.1
+  //   4096 tokens, 512 outputs (2048, 1)                    27.6 / 35.0, groups of 32 45.4 / 37.3
+  //   48 tokens, 65536 outputs (4096, 2)                    50.5 / 56.7, groups of 32 85.9 / 62.9
+  //   32 tokens, 65536 outputs (2048, 2)                    50.1 / 35.0, groups of 32 85.7 / 37.2
+  //   64 tokens, 151936 outputs (9496, 5)                   130 / 158, groups of 32 225 / 178
+  // and with 8192 inputs, 200 tokens, 8621 outputs (1890, 1) 91.6 / 122; with 512
+  // inputs, 160 tokens, 10078 outputs (1575, 1) 10.7 / 11.9.
+  const int64_t wgs = static_cast<int64_t>(np) * ((T + 31) / 32), rounds = (static_cast<int64_t>(nt) * nr + 255) / 256;
+  if (wgs > rounds * (G == 32 ? 2560 : 1600)) {
     const dim3 grid((nr * nt + 7) / 8 * 8), block(512);
     if (G == 32) hipLaunchKernelGGL((k_linear_tile<ACT, RES, true>), grid, block, 0, s, packed, x, y, T, N, K, G, off);
     else hipLaunchKernelGGL((k_linear_tile<ACT, RES, false>), grid, block, 0, s, packed, x, y, T, N, K, G, off);

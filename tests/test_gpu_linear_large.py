@@ -44,3 +44,52 @@ def test_tiles_of_any_count(T, N, G):
     q = torch.stack([(words >> (4 * j)) & 15 for j in range(8)], -1).view(N, K)
     w = q * s.double().repeat_interleave(G, 1) + b.double().repeat_interleave(G, 1)
     assert torch.equal(y[:T].double(), x.double() @ w.t().contiguous()) and (y[T:] == 7.0).all()
+
+
+TILED = [  # T, K, N, G, act, res: enough rows and tokens for the tiles of 128 x 128
+    (300, 64, 8300, 32, "bf16", "f32"), (300, 192, 8300, 32, "f16", "bf16"), (1000, 1152, 2700, 32, "bf16", "f16"),
+    (130, 576, 16000, 64, "bf16", "f32"), (385, 640, 4200, 128, "f16", "f16"), (64, 128, 32000, 64, "f16", "f32"),
+    (40, 320, 30001, 64, "bf16", "bf16"), (129, 1152, 12800, 128, "bf16", "f32"),
+]
+
+
+@pytest.mark.parametrize("T,K,N,G,act,res", TILED, ids=lambda v: str(v))
+def test_tiles_exact_integers_and_random(T, K, N, G, act, res):
+    import numpy as np
+    import torch
+    from oracle import linear_oracle as lo
+    from test_gpu_linear import HALF_STEP, dt, make, run
+    rng = np.random.default_rng(T * 131 + K + N)
+    q = rng.integers(0, 16, (N, K))
+    s = rng.integers(1, 4, (N, K // G)).astype(np.float16)
+    b = rng.integers(-20, 4, (N, K // G)).astype(np.float16)
+    x = rng.integers(-2, 3, (T, K)).astype(np.float32)
+    got = run(make(K, N, G, act, q, s, b), torch.from_numpy(x).cuda().to(dt(act)), res, pad=2)
+    want = torch.from_numpy(lo.linear(x, q, s, b, G)).to(dt(res)).double().numpy()
+    assert np.array_equal(got, want)
+    s = (rng.uniform(0.2, 1.2, (N, K // G)) / 40).astype(np.float16)
+    b = (-7.5 * s * rng.uniform(0.8, 1.2, s.shape)).astype(np.float16)
+    xr = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).cuda().to(dt(act))
+    x64 = xr.double().cpu().numpy()
+    got = run(make(K, N, G, act, q, s, b), xr, res)
+    ref, tol = lo.linear(x64, q, s, b, G), lo.error_bound(x64, q, s, b, G)
+    tol = tol + HALF_STEP[res] * (np.abs(ref) + tol) + 2.0 ** -25   # the last term: half a step of fp16 subnormals
+    assert (np.abs(got - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("G", [32, 64])
+def test_nonfinite_tokens_of_a_tile_reach_their_own_row_only(G):
+    import numpy as np
+    import torch
+    from test_gpu_linear import make, run
+    rng = np.random.default_rng(4)
+    K, N, T = 256, 200, 16500
+    s = np.full((N, K // G), 0.01, np.float16)
+    lin = make(K, N, G, "bf16", rng.integers(0, 16, (N, K)), s, (-8 * s).astype(np.float16))
+    x = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).cuda().bfloat16()
+    clean = run(lin, x, "f32")
+    x[7, 3], x[T - 1, 0] = float("nan"), float("inf")
+    got = run(lin, x, "f32")
+    assert np.isnan(got[7]).all() and not np.isfinite(got[T - 1]).any()
+    keep = [t for t in range(T) if t not in (7, T - 1)]
+    assert np.array_equal(got[keep], clean[keep])
