@@ -974,13 +974,15 @@ size_t prefill_bytes(const moe_gdn_desc* d, int N) {
 // sequences with 32 heads of 128: 15.1 us against 18.8 with four rows to a
 // lane; of 4 sequences, past the limit: 22.6 against 20.6; of 64: 230 against 144).
 constexpr int kFewRows = 512;
-// From so many blocks (slots x value heads) on, a workgroup of k_gdn_blocks
-// takes two value heads of a key head, which share its loads and products; below,
-// the turns only lengthen the kernel's tail (us in all, two against one; 16 key
-// and 32 value heads of 128): 8192 tokens (4128 blocks) 307 / 319, 8 x 512 tokens
-// (2304) 123 / 119, 4096 tokens (2080) 136 / 140, 8 x 256 (1280) 77 / 74, 2048
-// tokens (1056) 80 / 76.
-constexpr int kManyBlocks = 4096;
+// With more blocks of tokens and value heads than the chip holds workgroups of
+// k_gdn_blocks (four on each of 256 compute units), a workgroup takes two value
+// heads of a key head, which share its loads and products; below, its turns only
+// make the one round longer.  us in all, one head against two, 16 key and 32
+// value heads of 128: 1024 tokens (512 blocks) 51.6 / 56.1, 2048 (1024) 82.8 /
+// 86.4, 8 x 256 (1024) 80.4 / 84.2, 3000 (1500) 117 / 113, 4096 (2048) 152 / 144,
+// 8 x 512 (2048) 144.5 / 144.9, 8192 (4096) 322 / 312; 4 and 16 heads: 4096
+// (1024) 123 / 128, 8192 (2048) 234 / 230.
+constexpr int kChipBlocks = 1024;
 
 template <int ACT>
 hipError_t launch_prefill(const GdnArgs& a, uint8_t* ws, hipStream_t s) {
@@ -995,7 +997,7 @@ hipError_t launch_prefill(const GdnArgs& a, uint8_t* ws, hipStream_t s) {
   }
   if (e != hipSuccess || a.N <= kShort) return e;
   const auto slots = static_cast<uint32_t>(prefill_slots(a.B, a.N));
-  const int per = a.Hv / a.Hk % 2 == 0 && static_cast<int64_t>(slots) * a.Hv >= kManyBlocks ? 2 : 1;
+  const int per = a.Hv / a.Hk % 2 == 0 && static_cast<int64_t>(a.N) / kBlock * a.Hv > kChipBlocks ? 2 : 1;
   hipLaunchKernelGGL(k_gdn_blocks<ACT>, dim3(slots, a.Hv / per), dim3(256), 0, s, a, ws, per);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
