@@ -11,8 +11,12 @@
  * their last bits between batches.  Each output is rounded once to out_dtype.
  *
  * Weights are laid out once on the device by moe_linear_pack.  A value
- * outside a type's range overflows to infinity as a conversion does; a
- * non-finite x[t] reaches y[t] only.  The conventions of moe.h hold
+ * outside a type's range overflows to infinity as a conversion does.  Sums are
+ * formed as 16 s (sum (1 + q/16) x) + (b - 16 s) (sum x) over up to 256 columns,
+ * two parts that nearly cancel: they need 512 max|x[t]| (1 + 16 max|s| + max|b|)
+ * within fp32's range (3.4e38), which every fp16 x and a bf16 x of up to 10^34
+ * with |s|, |b| of up to 3 have; beyond, y[t] may be infinite or NaN where the
+ * sum itself is not.  A non-finite x[t] reaches y[t] only.  The conventions of moe.h hold
  * (caller-owned device buffers, work on the given stream only, negative
  * status and moe_last_error on refusal, n_tokens == 0 a no-op).
  */

@@ -93,3 +93,23 @@ def test_nonfinite_tokens_of_a_tile_reach_their_own_row_only(G):
     assert np.isnan(got[7]).all() and not np.isfinite(got[T - 1]).any()
     keep = [t for t in range(T) if t not in (7, T - 1)]
     assert np.array_equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("T,N,G", [(3, 70, 128), (3, 70, 32), (300, 9000, 128), (300, 9000, 32)])
+def test_large_activations_whose_parts_cancel(T, N, G):
+    # 512 |x| (1 + 16 s + |b|) is just within fp32's range; the two parts of a
+    # group's sum are 30 times the result and more
+    import numpy as np
+    import torch
+    from oracle import linear_oracle as lo
+    from test_gpu_linear import make, run
+    K = 1024
+    rng = np.random.default_rng(N)
+    q = 7 + (np.arange(K) + np.arange(N)[:, None]) % 2
+    s, b = np.full((N, K // G), 0.01, np.float16), np.full((N, K // G), -0.075, np.float16)
+    x = torch.from_numpy(5e35 * (1 - 0.2 * rng.random((T, K)))).float().cuda().bfloat16()
+    x64 = x.double().cpu().numpy()
+    assert 512 * np.abs(x64).max() * (1 + 0.16 + 0.075) < 3.4e38
+    got = run(make(K, N, G, "bf16", q, s, b), x, "f32")
+    ref, tol = lo.linear(x64, q, s, b, G), lo.error_bound(x64, q, s, b, G)
+    assert (np.abs(got - ref) <= tol + 2.0 ** -24 * (np.abs(ref) + tol)).all()
