@@ -118,18 +118,19 @@ __device__ __forceinline__ void run_tokens(const GdnArgs& a, int b, int h, int t
 }
 
 // Sequences up to this length go token by token, longer ones in blocks (32
-// value heads of 128; token by token against blocks, us): 20 tokens 10.0
-// against 15.9 for one sequence, 33 against 41 for 8, 174 against 219 for 64;
-// 24 tokens 11.3 / 15.9, 38 / 41, 203 / 223; 32 tokens 14.1 / 15.9, 46 / 41,
-// 261 / 230.
+// value heads of 128; token by token against blocks, us): 20 tokens 11.1
+// against 16.4 for one sequence, 35 against 39 for 8, 173 against 243 for 64;
+// 24 tokens 12.5 / 16.5, 39.1 / 39.5, 201 / 242; 32 tokens 15.8 / 16.5, 48 / 40,
+// 256 / 245.
 constexpr int kShort = 24;
 
 // The sequences of at most kShort tokens: one workgroup per (16 NS state rows,
 // value head, sequence).  With NS = 1 most of a token's arithmetic is the
 // conversion and the norms of its q and k, the same in every row; 4 rows per
-// lane share it.  64 sequences of 8 tokens with 32 heads of 128: 91 us, 268 MB
-// of state at 2.9 TB/s, bound by the vector arithmetic; 16 tokens of one
-// sequence: 6 us, bound by the latency of a token's chain of sums.
+// lane share it.  64 sequences of 8 tokens with 32 heads of 128: 97 us, 268 MB
+// of state at 2.8 TB/s, bound by the vector arithmetic; 16 tokens of one
+// sequence: 9.7 us with its launch, bound by the latency of a token's chain: its
+// norms, then its sums with the state.
 template <int ACT, int NS>
 __global__ __launch_bounds__(256) void k_gdn_tokens(GdnArgs a) {
   const int slices = (a.dv + 16 * NS - 1) / (16 * NS);
@@ -971,8 +972,8 @@ size_t prefill_bytes(const moe_gdn_desc* d, int N) {
 
 // Up to so many workgroups of 16 state rows (two for each compute unit) every
 // row has its own lanes: the chain of a token is shorter (16 tokens of 2
-// sequences with 32 heads of 128: 15.1 us against 18.8 with four rows to a
-// lane; of 4 sequences, past the limit: 22.6 against 20.6; of 64: 230 against 144).
+// sequences with 32 heads of 128: 16.6 us against 19.7 with four rows to a
+// lane; of 4 sequences, past the limit: 24.5 against 21.2; of 64: 241 against 148).
 constexpr int kFewRows = 512;
 // With more blocks of tokens and value heads than the chip holds workgroups of
 // k_gdn_blocks (four on each of 256 compute units), a workgroup takes two value
