@@ -303,11 +303,12 @@ __device__ __forceinline__ f32x4 mul16(float4 x, f32x4 y, f32x4 acc) {
 // blocks column by column, then block by block), which stays accurate also
 // where powers of A grow.
 //
-// 8192 tokens, 16 key and 32 value heads: 76 us (80 with one value head to a
-// workgroup), four workgroups to a compute unit; 205 MB of operands written at
-// 2.7 TB/s.  A lone workgroup with one value head takes about 9 us: loads and norms
+// 8192 tokens, 16 key and 32 value heads: 78 us (10 longer with one value head to
+// a workgroup), four workgroups to a compute unit; 205 MB of operands written at
+// 2.6 TB/s.  A lone workgroup with one value head takes about 9 us: loads and norms
 // a quarter, k.k and q.k with their decays a fifth, the inverse an eighth, T and
-// M a fifth, scaling and stores the rest.
+// M a fifth, scaling and stores the rest.  81 scalar registers are spilled to
+// lanes of vector registers (masks and addresses of the unrolled products).
 template <int ACT>
 __global__ __launch_bounds__(256, 4) void k_gdn_blocks(GdnArgs a, uint8_t* __restrict__ ws, int per) {
   __shared__ __attribute__((aligned(16))) uint16_t ks[kBlock * kRow];

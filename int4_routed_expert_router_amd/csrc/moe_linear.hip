@@ -357,8 +357,8 @@ __global__ __launch_bounds__(512, 2) void k_linear_tile(const uint8_t* __restric
 }
 
 // One thread per packed word (values), then one per 8-byte scale entry.  Once
-// per weight: 115.6 MB in 76 us (3.0 TB/s of reads and writes; the words of a
-// row are read 4 bytes at a time from 16 rows).  Workgroups in two dimensions: the
+// per weight: 115.6 MB in 76 us (3.0 TB/s of reads and writes, 114 us into fresh
+// memory; the words of a row are read 4 bytes at a time from 16 rows).  Workgroups in two dimensions: the
 // largest weights need more than the 2^32 threads that one holds.
 constexpr uint64_t kPackRow = 1 << 20;   // workgroups in the first dimension, at most
 __global__ __launch_bounds__(256) void k_linear_pack(const uint32_t* __restrict__ q, const uint16_t* __restrict__ s,

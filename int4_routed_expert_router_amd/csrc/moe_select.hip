@@ -13,8 +13,11 @@
 // 11 rounds that each take a maximum over the wave, and the fp64 scores of the
 // chosen.  64 tokens, 8 of 256 in 4 of 8 groups: 7.8 us.  8191 such tokens: 17.2
 // us, 8.9 MB at 0.5 TB/s, bound by the vector instructions of the rounds (four
-// tokens to a wave, 16 lanes each: 19.9 us against 21.7 for this form at that
-// time, and more than twice as long for few tokens; not kept).
+// tokens to a wave, 16 lanes each, were 19.9 us against 21.7 for this form when
+// all keys were fp64, and more than twice as long for few tokens; with the fp32
+// keys, or from a token count on, that form has not been tried).  Above 256
+// experts some scalar registers are spilled to lanes of vector registers (14 up
+// to 512, 70 up to 1024).
 #include <hip/hip_runtime.h>
 
 #include <cmath>
