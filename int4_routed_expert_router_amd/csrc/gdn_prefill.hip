@@ -188,7 +188,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 // Of a block that goes token by token (see k_gdn_scan) only kScGamma is set, to -1.
 constexpr size_t kKeyBytes = 48 * 1024;
 constexpr size_t kHeadBytes = 25 * 1024;
-constexpr int kScGamma = 192, kScInvT = 193, kScInvM = 194, kScGmax = 195, kScD0 = 196, kScD1 = 197, kScS0 = 198;
+constexpr int kScGamma = 192, kScInvT = 193, kScInvM = 194, kScGmax = 195, kScD = 196, kScS = 197;
 
 constexpr size_t kMaxSlots = (1 << 24) - 1;   // a grid dimension holds fewer than 2^32 threads, 256 per slot
 
@@ -493,18 +493,18 @@ __global__ __launch_bounds__(256, 4) void k_gdn_blocks(GdnArgs a, uint8_t* __res
       vec[128 + lane] = rqs[lane];
       // bounds on what the block makes of a state row of norm s and values up to
       // v (per state row), for the scales of the pairs: |R| <= v + gmax s,
-      // |e^(G_last - G) rk D| <= d0 v + d1 s, |S'| <= s0 v + gamma s.  They hold
-      // because the factors e^g (I - beta k k^T) have norm 1 at most (g <= 0,
-      // beta in [0, 2]) and rk <= 2^-12 (rows are scaled to a largest value of
-      // 2^12 or more).
-      const float gmax = wave_max(eg), bmax = wave_max(bt), dd = bmax * 0x1p-12f;
-      const float sg = wave_sum(bt * left), gamma = exp2_of(last);
+      // |e^(G_last - G) rk D| <= dd ((1 + sg) v + gamma s), |S'| <= sg v + gamma s.
+      // They hold because the factors e^g (I - beta k k^T) have norm 1 at most
+      // (g <= 0, beta in [0, 2]) and rk <= 2^-12 (rows are scaled to a largest
+      // value of 2^12 or more).  A decay below 2^-126 is 0 here, but not its
+      // products in T R: bounds take it as 2^-126.
+      const float gmax = wave_max(eg), dd = wave_max(bt) * 0x1p-12f;
+      const float sg = wave_sum(bt * fmaxf(left, 0x1p-126f)), gamma = exp2_of(last);
       if (lane == 0) {
         vec[kScGamma] = gamma;
         vec[kScGmax] = gmax;
-        vec[kScD0] = dd * (1.0f + sg);
-        vec[kScD1] = dd * gamma;
-        vec[kScS0] = sg;
+        vec[kScD] = dd;
+        vec[kScS] = sg;
       }
     }
     auto rows = [&](const float* m, int i, int k) {   // operand rows of block (i, k)
@@ -676,7 +676,8 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
   uint16_t va[4], vb[4];   // values of even and odd blocks
   float4 ev, rv;
   struct Scalars {
-    float4 a, b;   // kScGamma .. kScGmax, kScD0 .. kScS0
+    float4 a;   // kScGamma .. kScGmax
+    float2 b;   // kScD, kScS
     float4 eg;     // e^G rk of the lane's rows
   } sc0, sc1;      // of even and odd blocks
   const uint32_t lane16 = lane * 16;
@@ -690,7 +691,7 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
   };
   auto load_scalars = [&](const uint8_t* ph, Scalars& sc) {
     sc.a = *reinterpret_cast<const float4*>(ph + (24 * 1024 + 4 * kScGamma + zero));
-    sc.b = *reinterpret_cast<const float4*>(ph + (24 * 1024 + 4 * kScD0 + zero));
+    sc.b = *reinterpret_cast<const float2*>(ph + (24 * 1024 + 4 * kScD + zero));
     sc.eg = vec4(ph, 0);
   };
   auto load_keys = [&](const uint8_t* pk) {
@@ -790,8 +791,8 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
     const uint8_t* kn = more ? kp + kstep : kp;
     const uint8_t* hn = more ? hp + hstep : hp;
     load_scalars(hn, scnext);
-    const float gamma = sc.a.x, inv_t = sc.a.y, inv_m = sc.a.z, gmax = sc.a.w, cd0 = sc.b.x, cd1 = sc.b.y,
-                cs0 = sc.b.z;
+    const float gamma = sc.a.x, inv_t = sc.a.y, inv_m = sc.a.z, gmax = sc.a.w, dd = sc.b.x, sg = sc.b.y;
+    const float gbound = fmaxf(gamma, 0x1p-126f);
     float inv_s, fd, fo, inv_d, vs[4], as[4];
     // S pair
     {
@@ -815,11 +816,11 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
     // scales of R and D from the bounds; V and e^G rk under R's scale
     {
       const float vm = fmaxf(fmaxf(vmax[0][n], vmax[1][n]), fmaxf(vmax[2][n], vmax[3][n]));
-      const Pow2 pr = pow2_scale(fmaf(gmax, bound, vm)), pd = pow2_scale(fmaf(cd1, bound, cd0 * vm));
+      const Pow2 pr = pow2_scale(fmaf(gmax, bound, vm)), pd = pow2_scale(dd * fmaf(gbound, bound, fmaf(sg, vm, vm)));
       fd = inv_t * pd.up * pr.down;   // in this order: nothing on the way leaves fp32's range
       fo = inv_m * pr.down;
       inv_d = pd.down;
-      bound = cs0 * vm;   // the next block's, completed below
+      bound = sg * vm;   // the next block's, completed below
       const float at[4] = {sc.eg.x, sc.eg.y, sc.eg.z, sc.eg.w};
       // the two scales' product overflows only where every e^G of the block is
       // below fp32's normal numbers (and v is 0): a finite factor keeps 0 x it 0
@@ -898,7 +899,7 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
       df[w >> 1][1][lane][w & 1] = dl;
     }
     const float ss = (ssum[0][n] + ssum[1][n]) + (ssum[2][n] + ssum[3][n]);
-    bound = fmaf(gamma * inv_s, __builtin_amdgcn_sqrtf(ss), bound);
+    bound = fmaf(gbound * inv_s, __builtin_amdgcn_sqrtf(ss), bound);
     load_queries(kn);
     load_t(hn);
     if (more) prepare_values(c + 1, vnext);

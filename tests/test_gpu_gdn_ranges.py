@@ -265,3 +265,26 @@ def test_overflowing_rows_of_both_kinds_and_large_states(lens):
     d["k"][8, 0, 0] = zero["k"][8, 0, 0] = 3e38   # one element alone
     zero["k"][8] = 0
     hold(d, lens, "bf16", want=zero)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("size", [1e6, 1e15, 1e30])
+def test_large_states_that_decay_past_fp32s_smallest_number(size, act):
+    # e^G of a block passes 2^-126 after 4 to 60 tokens, in another token for
+    # every head; rows without values, which then have no other size to go by.
+    # The floor is that of test_what_a_block_shrinks_beyond_its_digits
+    import torch
+    lens = [150, 65]
+    d = inputs(lens, 1, 16, 48, act, 43)
+    d["state"] *= size
+    d["v"][..., ::3] = 0
+    d["g"][:] = -87.4 / torch.linspace(4.0, 60.0, 16)
+    d["g"][:, ::5] -= 0.05 * d["beta"][:, ::5]
+    d["beta"][:, 3] *= 1e-20
+    d["beta"][:, 4] = 1e-40
+    got_o, got_s = (x.astype(np.float64) for x in gpu(d, lens, act))
+    o, S, bo, bs = oracle_with_bounds(d, lens)
+    assert np.isfinite(got_o).all() and np.isfinite(got_s).all()
+    floor = 2.0 ** -40 * np.linalg.norm(d["state"].double().numpy(), axis=(-1, -2)).max()
+    assert (np.linalg.norm(got_o - o, axis=-1) <= bo + Q_SCALE * floor).all()
+    assert (np.sqrt(((got_s - S) ** 2).sum((-1, -2))) <= bs + floor).all()
