@@ -72,7 +72,7 @@ moe_status moe_gdn_step(const moe_gdn_desc* desc, const void* q, const void* k, 
  * State and sums are fp32; the results are those of the tokens taken one by one
  * up to fp32 rounding (in a block of 64 tokens, see below, also up to 2^-40 of
  * the block's largest value and of the state before it: what a block shrinks
- * further than that may become 0), bitwise repeatable, and a sequence's results
+ * further than that may become 0, for the tokens after it too), bitwise repeatable, and a sequence's results
  * do not depend on the other sequences.  Any g and beta work whose states stay in
  * fp32's range (g = -inf clears the state), but g <= 0 and beta in [0, 2] are
  * expected: with more than 24 tokens, a sequence and value head is taken in

@@ -936,7 +936,8 @@ __global__ __launch_bounds__(256, 2) void k_gdn_scan(GdnArgs a, const uint8_t* _
     const int left = t1 - (t0 + c * kBlock + 16 * w);   // uniform
     float v[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) v[r] = rt[r] * fmaf(et[r] * inv_s, Y[r], fo * fmaf(kLoDown, O1[r], O[r]));
+    for (int r = 0; r < 4; ++r)   // the row's norm first: its products are some 2^16 times the result
+      v[r] = fmaf(rt[r] * Y[r], et[r] * inv_s, rt[r] * fmaf(kLoDown, O1[r], O[r]) * fo);
     if (left >= 16) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) *(op + r * row_el + el) = v[r];

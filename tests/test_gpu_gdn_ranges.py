@@ -223,7 +223,7 @@ def uneven(edit, d, lens):
 
 @pytest.mark.parametrize("lens", LENS + [[70, 3, 129, 64]], ids=IDS + ["batch"])
 @pytest.mark.parametrize("edit", ["jump", "large 0.2", "large 0.5", "large 2", "novalues 0.05", "novalues 0.2", "values",
-                                  "betas", "tail", "all 1e-34"])
+                                  "betas", "tail", "all 1e-34", "all 1e36"])
 def test_numbers_of_very_different_size_in_a_block(lens, edit):
     d = inputs(lens, 2, 4, 48, "bf16", 37)
     uneven(edit, d, lens)
