@@ -72,14 +72,15 @@ moe_status moe_gdn_step(const moe_gdn_desc* desc, const void* q, const void* k, 
  * State and sums are fp32; the results are those of the tokens taken one by one
  * up to fp32 rounding (in a block of 64 tokens, see below, also up to 2^-40 of
  * the block's largest value and of the state before it: what a block shrinks
- * further than that may become 0, for the tokens after it too), bitwise repeatable, and a sequence's results
- * do not depend on the other sequences.  Any g and beta work whose states stay in
- * fp32's range (g = -inf clears the state), but g <= 0 and beta in [0, 2] are
- * expected: with more than 24 tokens, a sequence and value head is taken in
- * blocks of 64 tokens up to its first block with another g or beta, and token by
- * token, some 15 times slower, from there on.  A non-finite k, v, beta or g makes
- * that sequence's results unusable from the start of its 64-token block on.  A
- * row of q or k whose sum of squares overflows fp32 counts as zero. */
+ * further than that may become 0, for the tokens after it too), bitwise
+ * repeatable, and a sequence's results do not depend on the other sequences.
+ * Any g and beta work whose states stay in fp32's range (g = -inf clears the
+ * state), but g <= 0 and beta in [0, 2] are expected: with more than 24 tokens,
+ * a sequence and value head is taken in blocks of 64 tokens up to its first
+ * block with another g or beta, and token by token, some 15 times slower, from
+ * there on.  A non-finite k, v, beta or g makes that sequence's results unusable
+ * from the start of its 64-token block on.  A row of q or k whose sum of squares
+ * overflows fp32 counts as zero. */
 moe_status moe_gdn_prefill_workspace_bytes(const moe_gdn_desc* desc, int32_t n_tokens, size_t* bytes);
 moe_status moe_gdn_prefill(const moe_gdn_desc* desc, const int32_t* seq_off, int32_t n_tokens, const void* q,
                            const void* k, const void* v, const float* g, const float* beta, float q_scale,
