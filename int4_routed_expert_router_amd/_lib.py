@@ -50,6 +50,19 @@ class LinearDesc(C.Structure):
                 ("out_dtype", C.c_int32)]
 
 
+class AttnDesc(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("q_heads", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("act_dtype", C.c_int32), ("page_size", C.c_int32), ("n_pages", C.c_int32), ("max_pages", C.c_int32)]
+
+
+class KvCacheC(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("table", C.c_void_p), ("length", C.c_void_p)]
+
+
+class AttnRows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
 class SlotPoolConfig(C.Structure):
     _fields_ = [("n_layers", C.c_int32), ("n_experts", C.c_int32), ("slots_per_layer", C.c_int32),
                 ("aging_period", C.c_int32), ("blob_stride", C.c_uint64), ("blob_bytes", C.c_uint64),
@@ -102,6 +115,10 @@ PROTOS = {
     "moe_gdn_step": (i32, [C.POINTER(GdnDesc), vp, vp, vp, vp, vp, f32, vp, vp, vp]),
     "moe_gdn_prefill_workspace_bytes": (i32, [C.POINTER(GdnDesc), i32, C.POINTER(C.c_size_t)]),
     "moe_gdn_prefill": (i32, [C.POINTER(GdnDesc), vp, i32, vp, vp, vp, vp, vp, f32, vp, vp, vp, C.c_size_t, vp]),
+    "moe_kv_append": (i32, [vp, vp, vp, i32, vp, vp, vp, vp, vp, vp, f32, vp, i32, vp]),
+    "moe_attn_workspace_bytes": (i32, [vp, i32, C.POINTER(C.c_size_t)]),
+    "moe_attn_decode": (i32, [vp, vp, vp, vp, f32, vp, vp, C.c_size_t, vp]),
+    "moe_attn_prefill": (i32, [vp, vp, vp, i32, vp, vp, f32, vp, vp, C.c_size_t, vp]),
     "slotpool_create": (i32, [C.POINTER(SlotPoolConfig), C.POINTER(vp)]),
     "slotpool_acquire": (i32, [vp, i32, vp, i32, u64, vp, vp, vp, vp]),
     "slotpool_prefetch": (i32, [vp, i32, vp, i32, u64, vp, vp, vp, vp, vp]),

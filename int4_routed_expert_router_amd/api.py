@@ -14,7 +14,7 @@ import dataclasses
 import numpy as np
 import torch
 
-from ._lib import (GdnDesc, LinearDesc, MOE_BF16, MOE_F16, MOE_F32, MOE_PATH_AUTO, MOE_POOL_DMA_COPY, MOE_POOL_HOST_ONLY, LayerDesc,  # noqa: F401
+from ._lib import (AttnDesc, AttnRows, GdnDesc, KvCacheC, LinearDesc, MOE_BF16, MOE_F16, MOE_F32, MOE_PATH_AUTO, MOE_POOL_DMA_COPY, MOE_POOL_HOST_ONLY, LayerDesc,  # noqa: F401
                    LayerWeights, MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, SelectDescC, SlotPoolConfig, SlotPoolStats,
                    check, lib)
 
@@ -23,7 +23,7 @@ __all__ = ["Desc", "Layer", "blob_bytes", "pack_expert", "workspace_bytes", "wor
            "expert_ffn", "layer_forward", "layer_forward_static", "stack_epilogue", "stack_forward", "StackGraph", "synth_fill_experts",
            "synth_philox", "SlotPool", "pool_decode_step", "DevPool", "pool_decode_step_dev", "PoolGraph", "gdn_step",
            "SelectDesc", "select", "route_scored", "Linear", "linear", "gdn_prefill",
-           "gdn_prefill_workspace"]
+           "gdn_prefill_workspace", "KVCache", "kv_append", "attn_workspace", "attn_decode", "attn_prefill"]
 
 
 _ACT = {"bf16": MOE_BF16, "f16": MOE_F16}
@@ -555,6 +555,141 @@ def gdn_prefill(q, k, v, g, beta, state, o, seq_off, q_scale, act_dtype="bf16", 
             ws = gdn_prefill_workspace(B, N, Hk, Hv, dv, act_dtype, dk, q.device)
     _call_on(dev, lib().moe_gdn_prefill, C.byref(d), *args, _arg(ws, "ws", (torch.uint8,), None, dev), ws.numel(),
              _stream_on(dev, stream))
+
+
+_ACT_OF = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16}
+
+
+class KVCache:
+    """Paged key-value cache of one attention layer: the caller's tensors, read
+    and written in place (include/moe_attn.h).
+
+    k, v: [n_pages, kv_heads, page_size, head_dim] float16 or bfloat16; table:
+    [B, max_pages] int32, the pages of each sequence in order (an entry outside
+    [0, n_pages): no page); length: [B] int32, each sequence's tokens, those of
+    the call included.  All contiguous, on one GPU; table and length may change
+    between calls, also between replays of a captured one."""
+
+    def __init__(self, k, v, table, length):
+        dev = _device(k, "k")
+        if k.dim() != 4 or k.dtype not in _ACT_OF:
+            raise ValueError("k must be a float16 or bfloat16 tensor [n_pages, kv_heads, page_size, head_dim]")
+        if not isinstance(v, torch.Tensor) or v.shape != k.shape:
+            raise ValueError("v must have k's shape")
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table must be a tensor of 2 dimensions")
+        if not isinstance(length, torch.Tensor) or length.shape != table.shape[:1]:
+            raise ValueError("length must be a tensor [B]")
+        for t, name, dtypes in ((k, "k", (k.dtype,)), (v, "v", (k.dtype,)), (table, "table", _I32),
+                                (length, "length", _I32)):
+            _arg(t, name, dtypes, None, dev)
+        self.k, self.v, self.table, self.length = k, v, table, length
+        self.n_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        self.batch, self.max_pages = table.shape
+        self._dev = dev
+        self._desc = {}
+
+    def desc(self, q_heads):
+        """The call's shape for q_heads query heads."""
+        d = self._desc.get(q_heads)
+        if d is None:
+            d = self._desc[q_heads] = AttnDesc(self.batch, q_heads, self.kv_heads, self.head_dim,
+                                               _ACT_OF[self.k.dtype], self.page_size, self.n_pages, self.max_pages)
+        return d
+
+    def _c(self):
+        return KvCacheC(self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(), self.length.data_ptr())
+
+    def _rows(self, t, name, shape=None):
+        """Strided rows [T, heads, head_dim] for the C ABI."""
+        if t is None:
+            return None
+        if _device(t, name) != self._dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{self._dev}")
+        if t.dim() != 3 or t.shape[2] != self.head_dim or (shape is not None and t.shape != shape):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                             f"{tuple(shape) if shape is not None else ('T', 'heads', self.head_dim)}")
+        if t.dtype != self.k.dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {self.k.dtype}")
+        st, sh, sd = t.stride()
+        if sd != 1:
+            raise ValueError(f"{name}: the values of a head must lie next to each other")
+        # the stride of a dimension of one is never used
+        return AttnRows(t.data_ptr(), st if t.shape[0] > 1 else 0, sh if t.shape[1] > 1 else 0)
+
+    def _out(self, t, name, shape):
+        p = _arg(t, name, (self.k.dtype,), None, self._dev)
+        if p is None or t.shape != shape:
+            raise ValueError(f"{name} must be a tensor of shape {tuple(shape)}")
+        return p
+
+
+def _ref(c):
+    return None if c is None else C.byref(c)
+
+
+def kv_append(cache, k, v, seq_off=None, q=None, q_out=None, q_norm=None, k_norm=None, eps=1e-6, freq=None,
+              stream=None):
+    """New tokens' keys and values [N, kv_heads, head_dim] into the cache's
+    pages (moe_kv_append), the last positions of their sequences: rows
+    seq_off[b] .. seq_off[b+1] - 1 (int32 [B+1] on the device; None: one token
+    for each sequence).  With q [N, q_heads, head_dim] also q_out, the queries
+    with their norms and positions.  q_norm, k_norm: fp32 [head_dim] or None;
+    freq: fp64 [rot_dim / 2] radians per position or None.  k, v and q may be
+    slices of wider rows (strides in multiples of 8)."""
+    kr = cache._rows(k, "k")
+    if k.shape[1] != cache.kv_heads:
+        raise ValueError(f"k has {k.shape[1]} heads, expected {cache.kv_heads}")
+    N, dev, D = k.shape[0], cache._dev, cache.head_dim
+    vr, qr = cache._rows(v, "v", k.shape), cache._rows(q, "q")
+    if q is not None and q.shape[0] != N:
+        raise ValueError(f"q has {q.shape[0]} tokens, expected {N}")
+    if q is None and q_out is not None:
+        raise ValueError("q_out needs q")
+    _call_on(dev, lib().moe_kv_append, C.byref(cache.desc(cache.kv_heads if q is None else q.shape[1])),
+             C.byref(cache._c()), _arg(seq_off, "seq_off", _I32, cache.batch + 1, dev), N, C.byref(kr), C.byref(vr),
+             _ref(qr), None if q is None else cache._out(q_out, "q_out", q.shape),
+             _arg(q_norm, "q_norm", _F32, D, dev), _arg(k_norm, "k_norm", _F32, D, dev), float(eps),
+             _arg(freq, "freq", (torch.float64,), None, dev), 0 if freq is None else 2 * freq.numel(),
+             _stream_on(dev, stream))
+
+
+def attn_workspace(cache, q_heads, n_tokens=None):
+    """Workspace of attn_decode (n_tokens None) and attn_prefill of up to n_tokens tokens."""
+    n = C.c_size_t(0)
+    check(lib().moe_attn_workspace_bytes(C.byref(cache.desc(q_heads)), n_tokens or 0, C.byref(n)))
+    return torch.empty(max(int(n.value), 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def _attend(cache, q, o, gate, ws, stream, decode):
+    qr = cache._rows(q, "q")
+    gr = cache._rows(gate, "gate", q.shape)
+    op = cache._out(o, "o", q.shape)
+    if ws is None:
+        with _allocating_on(stream):
+            ws = attn_workspace(cache, q.shape[1], None if decode else q.shape[0])
+    return (C.byref(cache.desc(q.shape[1])), C.byref(cache._c())), (C.byref(qr), _ref(gr)), (
+        op, _arg(ws, "ws", (torch.uint8,), None, cache._dev), ws.numel(), _stream_on(cache._dev, stream))
+
+
+def attn_decode(cache, q, o, scale, gate=None, ws=None, stream=None):
+    """Attention of the last token of every sequence over its cached positions
+    (moe_attn_decode): q, gate (or None) [B, q_heads, head_dim], which may be
+    slices of wider rows, o [B, q_heads, head_dim]."""
+    head, rows, tail = _attend(cache, q, o, gate, ws, stream, True)
+    if q.shape[0] != cache.batch:
+        raise ValueError(f"q has {q.shape[0]} tokens, expected one for each of {cache.batch} sequences")
+    _call_on(cache._dev, lib().moe_attn_decode, *head, *rows, float(scale), *tail)
+
+
+def attn_prefill(cache, q, o, seq_off, scale, gate=None, ws=None, stream=None):
+    """Causal attention of the last tokens of every sequence (moe_attn_prefill):
+    q, gate (or None) [N, q_heads, head_dim], which may be slices of wider rows,
+    rows seq_off[b] .. seq_off[b+1] - 1 (int32 [B+1] on the device) being the
+    last positions of sequence b; o [N, q_heads, head_dim]."""
+    head, rows, tail = _attend(cache, q, o, gate, ws, stream, False)
+    _call_on(cache._dev, lib().moe_attn_prefill, *head, _arg(seq_off, "seq_off", _I32, cache.batch + 1, cache._dev),
+             q.shape[0], *rows, float(scale), *tail)
 
 
 _OUT = {torch.float16: MOE_F16, torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}

@@ -1,0 +1,80 @@
+// What the attention kernels and their entry points share (see include/moe_attn.h).
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "moe_attn.h"
+#include "moe_common.h"
+
+namespace moe {
+
+struct AttnArgs {
+  const uint16_t *k, *v;        // cache
+  const int32_t *table, *length, *off;
+  const uint16_t *q, *gate;     // gate or nullptr
+  int64_t q_ts, q_hs, g_ts, g_hs;   // token and head strides, elements
+  uint16_t* o;
+  float scale;
+  int B, N, Hq, Hk, page_log, n_pages, max_pages;
+};
+
+struct AppendArgs {
+  uint16_t *kc, *vc;
+  const int32_t *table, *length, *off;   // off nullptr: token t is sequence t's only one
+  const uint16_t *k, *v, *q;             // q or nullptr
+  int64_t k_ts, k_hs, v_ts, v_hs, q_ts, q_hs;
+  uint16_t* q_out;
+  const float *q_norm, *k_norm;
+  const double* freq;
+  float eps;
+  int rot, B, N, Hq, Hk, page_log, n_pages, max_pages;
+};
+
+// Two values rounded to nearest even, the first in the low half.
+template <int ACT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (ACT == 2) return __builtin_bit_cast(uint32_t, bf16x2_t{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+  else return __builtin_bit_cast(uint32_t, f16x2_t{static_cast<_Float16>(a), static_cast<_Float16>(b)});
+}
+
+// tokens of sequence b in the cache, the new ones included
+__device__ __forceinline__ int seq_length(const int32_t* length, int b, int max_pages, int page_log) {
+  return min(max(length[b], 0), max_pages << page_log);
+}
+
+// Rows [begin, end) of sequence b, with the offsets forced into [0, N].
+__device__ __forceinline__ void seq_rows(const int32_t* off, int b, int N, int& begin, int& end) {
+  begin = min(max(off[b], 0), N);
+  end = max(min(max(off[b + 1], 0), N), begin);
+}
+
+// The sequence that owns row t (wave-uniform; B where none does): a search
+// that takes 64 offsets at a time, one to a lane, so that up to 64 sequences
+// cost one load and 4096 two.  The answer is checked against the range that it
+// names, so offsets in any order only leave rows without an owner.
+__device__ __forceinline__ int seq_of_row(const int32_t* off, int B, int N, int t) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = B;   // candidates lo .. lo + n - 1: the last b with off[b] <= t and b < B that owns rows
+  while (n > 64) {
+    const int step = (n + 63) / 64, i = lo + lane * step;
+    const uint64_t le = __ballot(i < lo + n && off[min(i, B)] <= t);
+    if (le == 0) return B;
+    const int last = 63 - __builtin_clzll(le);
+    const int from = lo + last * step;
+    n = min(step, lo + n - from);
+    lo = from;
+  }
+  const uint64_t le = __ballot(lane < n && off[min(lo + lane, B)] <= t);
+  if (le == 0) return B;
+  const int b = lo + 63 - __builtin_clzll(le);
+  int begin, end;
+  seq_rows(off, b, N, begin, end);
+  return t >= begin && t < end ? b : B;
+}
+
+hipError_t launch_kv_append(int act, int d, const AppendArgs& a, hipStream_t s);
+size_t attn_decode_bytes(const moe_attn_desc* d);
+size_t attn_prefill_bytes(const moe_attn_desc* d, int N);
+hipError_t launch_attn_decode(int act, int d, const AttnArgs& a, void* ws, hipStream_t s);
+hipError_t launch_attn_prefill(int act, int d, const AttnArgs& a, void* ws, hipStream_t s);
+
+}  // namespace moe

@@ -21,6 +21,8 @@ explainer, "How Expert Streaming Works"):
 * ``deltanet_oracle`` - Gated DeltaNet, one token and over whole sequences.
 * ``linear_oracle`` - dense int4 affine products and the bound on their fp32 sums.
 * ``select_oracle`` - scored, biased and group-limited expert choice.
+* ``attention_oracle`` - attention over a paged key-value cache, the append to
+  the cache, and the bound on the error of fp32 arithmetic.
 
 Every function works in float64 unless it models a rounding step the method
 itself defines (bf16 round-to-nearest-even of the next layer's input).
