@@ -67,7 +67,10 @@ extern "C" {
  * page_size: 16, 32, 64, 128 or 256
  * n_pages:   >= 1
  * max_pages: >= 1, max_pages * page_size up to 2^30 and batch * kv_heads *
- *            max_pages * page_size up to 2^37 */
+ *            max_pages * page_size up to 2^37
+ * Calls that take n_tokens hold up to 2^22 blocks of 256 / (q_heads / kv_heads)
+ * (rounded down) tokens: kv_heads * (n_tokens / block + batch), where a batch
+ * above n_tokens counts as n_tokens. */
 typedef struct {
   int32_t batch, q_heads, kv_heads, head_dim, act_dtype, page_size, n_pages, max_pages;
 } moe_attn_desc;

@@ -49,6 +49,23 @@ __device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
+template <int ACT>
+__device__ __forceinline__ f32x16_t mfma32(uint4 a, uint4 b, f32x16_t c) {
+  if constexpr (ACT == 2)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+// Maximum and sum over the two lanes l, l ^ 32.
+__device__ __forceinline__ float pair_max(float v) {
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_int(v), __float_as_int(v), false, false);
+  return fmaxf(__int_as_float(b[0]), __int_as_float(b[1]));
+}
+__device__ __forceinline__ float pair_sum(float v) {
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_int(v), __float_as_int(v), false, false);
+  return __int_as_float(b[0]) + __int_as_float(b[1]);
+}
 // Maximum and sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48; identical bits in each.
 __device__ __forceinline__ float quad_max(float v) {
   const auto a = __builtin_amdgcn_permlane16_swap(__float_as_int(v), __float_as_int(v), false, false);
@@ -108,6 +125,7 @@ __device__ __forceinline__ int seq_of_row(const int32_t* off, int B, int N, int 
 }
 
 hipError_t launch_kv_append(int act, int d, const AppendArgs& a, hipStream_t s);
+bool attn_prefill_fits(const moe_attn_desc* d, int N);   // whether a grid holds the call
 size_t attn_decode_bytes(const moe_attn_desc* d);
 size_t attn_prefill_bytes(const moe_attn_desc* d, int N);
 hipError_t launch_attn_decode(int act, int d, const AttnArgs& a, void* ws, hipStream_t s);

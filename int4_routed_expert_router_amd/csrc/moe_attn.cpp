@@ -35,6 +35,9 @@ moe_status check_desc(const moe_attn_desc* d, int32_t n_tokens) {
     return set_error(MOE_ESHAPE, "batch * kv_heads * max_pages * page_size must be at most 2^37");
   if (n_tokens < 0 || n_tokens > kMaxTokens)
     return set_error(MOE_ESHAPE, "n_tokens=%d must be in [0, 2^20]", n_tokens);
+  if (!attn_prefill_fits(d, n_tokens))
+    return set_error(MOE_ESHAPE, "n_tokens=%d of %d sequences and %d key heads are more than a launch holds", n_tokens,
+                     d->batch, d->kv_heads);
   return MOE_OK;
 }
 
