@@ -31,6 +31,7 @@ constexpr int kShareLog = 8;                // shares of the whole: the compute 
 constexpr int kSlots = 2 << kShareLog;      // chunks of cut units: below 2 tiles / share size
 constexpr int kMinChunk = 4;                // tiles
 constexpr int kMaxUnits = 1 << 22;
+constexpr int kAhead = 4;                   // operands in flight from LDS
 
 struct Unit {     // uniform
   int b, h, begin, n, base;   // sequence, key head, first row, tokens, positions before them (may be negative)
@@ -201,11 +202,17 @@ __device__ Unit find_unit(const AttnArgs& a, uint32_t item, int tpb, int* n_part
   return u;
 }
 
-typedef __attribute__((address_space(3))) void lds_void;
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
-__device__ __forceinline__ void to_lds16(const void* g, void* lds) {
-  __builtin_amdgcn_global_load_lds(g, (lds_void*)lds, 16, 0, 0);
+// 16 bytes a lane from base + at to LDS address lds + 16 lane, behind the
+// compiler's back: it would wait for every such copy before the next LDS read,
+// whichever buffer that reads.  landed() waits for the wave's own.
+__device__ __forceinline__ void to_lds16(const void* base, uint32_t at, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(at), "s"(base), "s"(lds) : "memory", "m0");
+}
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)(p)));
 }
 // Two values of each of 4 rows, transposed: lanes 4 r .. 4 r + 3 of 16 point at row r.
 __device__ __forceinline__ uint2 read_transposed(const uint8_t* p) {
@@ -236,7 +243,7 @@ template <int ACT, int D>
 __global__ __launch_bounds__(64 * Shape<D>::kWaves, 2) void k_attn_prefill(AttnArgs a, uint8_t* ws) {
   constexpr int kT = Shape<D>::kTiles, kW = Shape<D>::kWaves, kBytes = Shape<D>::kTileBytes;
   constexpr int kSteps = D / 16, kBlocks = D / 32, kPieces = D / 8;   // 16-byte pieces of a row
-  constexpr int kLoadKeys = 64 / kPieces * 1, kLoads = kKeys / (kLoadKeys * kW);
+  constexpr int kLoadKeys = 64 / kPieces, kLoads = kKeys / (kLoadKeys * kW);
   __shared__ __align__(1024) uint8_t tiles[2][2][kBytes];   // buffer, keys and values
   __shared__ int bad_key[2];
   const int lane = threadIdx.x & 63, l32 = lane & 31, hf = lane >> 5, group = a.Hq / a.Hk, tpb = kRows / group;
@@ -299,19 +306,21 @@ __global__ __launch_bounds__(64 * Shape<D>::kWaves, 2) void k_attn_prefill(AttnA
     pages = id < a.n_pages ? id : -1;
     live = __ballot(pages >= 0);
   };
-  const int load_key = lane / kPieces, load_piece = lane % kPieces;
+  // this lane's 16 bytes of a load: a key's place in its group of 16 is the same in all loads of a wave
+  const int load_key = lane / kPieces, in_group = (wave * kLoadKeys & 15) + load_key;
+  const int v_swz = D == 64 ? (in_group >> 1) & 1 : in_group & (D / 32 - 1);   // values: 64-byte groups of pieces
+  const uint32_t k_at = 2 * (in_group * D + 8 * (lane % kPieces ^ (in_group & 7)));
+  const uint32_t v_at = 2 * (in_group * D + 8 * (lane % kPieces ^ v_swz << 2));
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(&tiles[0][0][wave * 1024]));
   auto issue = [&](int t, int buf) {
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int k0 = (i * kW + wave) * kLoadKeys, g = k0 >> 4, p = (t << kKeysLog) + 16 * g;
+      const int g = (i * kW + wave) * kLoadKeys >> 4, p = (t << kKeysLog) + 16 * g;
       const int id = max(__builtin_amdgcn_readlane(pages, 4 * (t & 15) + g), 0);
       const size_t at = (((static_cast<size_t>(id) * a.Hk + u.h) << a.page_log) + (p & ((1 << a.page_log) - 1))) * D;
-      const int key = k0 + load_key;
-      const uint32_t row = ((key & 15) * D);
-      to_lds16(a.k + at + row + 8 * (load_piece ^ (key & 7)), &tiles[buf][0][k0 * D * 2]);
-      // values: 64-byte groups of pieces
-      const int swz = D == 64 ? (key >> 1) & 1 : key & (D / 32 - 1);
-      to_lds16(a.v + at + row + 8 * (load_piece ^ (swz << 2)), &tiles[buf][1][k0 * D * 2]);
+      const uint32_t lds = lds0 + buf * 2 * kBytes + i * kW * 1024;
+      to_lds16(a.k + at, k_at, lds);
+      to_lds16(a.v + at, v_at, lds + kBytes);
     }
   };
   if (threadIdx.x == 0) bad_key[0] = bad_key[1] = INT_MAX;
@@ -320,7 +329,7 @@ __global__ __launch_bounds__(64 * Shape<D>::kWaves, 2) void k_attn_prefill(AttnA
   int alive = (live >> (4 * (t_first & 15))) & 15;
   for (int t = t_first; t < t_last; ++t) {
     const int buf = (t - t_first) & 1;
-    __builtin_amdgcn_s_waitcnt(0);
+    landed();
     __syncthreads();   // tile t has landed, and all are done with tile t - 1
     const int alive_now = alive;
     if (t + 1 < t_last) {
@@ -366,13 +375,25 @@ __global__ __launch_bounds__(64 * Shape<D>::kWaves, 2) void k_attn_prefill(AttnA
       for (int r = 0; r < kT; ++r)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[r][i] = 0;
+      // Operands are read kAhead products before they are used.
       const uint8_t* kp = &tiles[buf][0][(32 * sub + l32) * D * 2];
+      auto key_part = [&](int i) { return *reinterpret_cast<const uint4*>(kp + (((2 * i + hf) ^ (lane & 7)) << 4)); };
+      uint4 kf[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) kf[i] = key_part(i);
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const uint4 k = *reinterpret_cast<const uint4*>(kp + (((2 * i + hf) ^ (lane & 7)) << 4));
 #pragma unroll
-        for (int r = 0; r < kT; ++r) s[r] = mfma32<ACT>(k, q[r][i], s[r]);
+        for (int r = 0; r < kT; ++r) s[r] = mfma32<ACT>(kf[i % kAhead], q[r][i], s[r]);
+        if (i + kAhead < kSteps) kf[i % kAhead] = key_part(i + kAhead);
       }
+      __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+      for (int i = kAhead; i < kSteps; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, kT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x8, kT * kAhead, 0);
       if (key0 + 31 > low || alive_now != 15) {
 #pragma unroll
         for (int r = 0; r < kT; ++r)
@@ -422,17 +443,27 @@ __global__ __launch_bounds__(64 * Shape<D>::kWaves, 2) void k_attn_prefill(AttnA
       const int vk = 4 * hf + ((lane >> 2) & 3);
       const uint8_t* vp = &tiles[buf][1][(32 * sub + vk) * D * 2 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8];
       const int swz = D == 64 ? (vk >> 1) & 1 : vk & (D / 32 - 1);
+      auto value_part = [&](int n) {
+        const uint8_t* vi = vp + ((n >> 1 ^ swz) << 6) + 16 * (n & 1) * D * 2;
+        const uint2 x = read_transposed(vi), y = read_transposed(vi + 8 * D * 2);
+        return make_uint4(x.x, x.y, y.x, y.y);
+      };
+      uint4 vf[kAhead];
 #pragma unroll
-      for (int i = 0; i < kBlocks; ++i) {
-        const uint8_t* vi = vp + ((i ^ swz) << 6);
+      for (int n = 0; n < kAhead; ++n) vf[n] = value_part(n);
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2) {
-          const uint2 x = read_transposed(vi + 16 * h2 * D * 2), y = read_transposed(vi + (16 * h2 + 8) * D * 2);
-          const uint4 v = make_uint4(x.x, x.y, y.x, y.y);
+      for (int n = 0; n < 2 * kBlocks; ++n) {
 #pragma unroll
-          for (int r = 0; r < kT; ++r) o[r][i] = mfma32<ACT>(v, p[r][h2], o[r][i]);
-        }
+        for (int r = 0; r < kT; ++r) o[r][n >> 1] = mfma32<ACT>(vf[n % kAhead], p[r][n & 1], o[r][n >> 1]);
+        if (n + kAhead < 2 * kBlocks) vf[n % kAhead] = value_part(n + kAhead);
       }
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * kAhead, 0);
+#pragma unroll
+      for (int n = kAhead; n < 2 * kBlocks; ++n) {
+        __builtin_amdgcn_sched_group_barrier(0x8, kT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x8, kT * kAhead, 0);
     }
   }
 
