@@ -82,7 +82,7 @@ typedef struct {
 } moe_kv_cache;
 
 /* Rows of a call: head h of token t starts at data + t * token_stride + h *
- * head_stride (elements; both multiples of 8, >= 0) and is head_dim values
+ * head_stride (elements; both multiples of 8 in [0, 2^31)) and is head_dim values
  * long; 16-byte aligned.  So a slice of a wider projection's output can be
  * taken as it is. */
 typedef struct {

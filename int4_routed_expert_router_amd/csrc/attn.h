@@ -11,7 +11,7 @@ struct AttnArgs {
   const uint16_t *k, *v;        // cache
   const int32_t *table, *length, *off;
   const uint16_t *q, *gate;     // gate or nullptr
-  int64_t q_ts, q_hs, g_ts, g_hs;   // token and head strides, elements
+  int32_t q_ts, q_hs, g_ts, g_hs;   // token and head strides, elements
   uint16_t* o;
   float scale;
   int B, N, Hq, Hk, page_log, n_pages, max_pages;
@@ -21,7 +21,7 @@ struct AppendArgs {
   uint16_t *kc, *vc;
   const int32_t *table, *length, *off;   // off nullptr: token t is sequence t's only one
   const uint16_t *k, *v, *q;             // q or nullptr
-  int64_t k_ts, k_hs, v_ts, v_hs, q_ts, q_hs;
+  int32_t k_ts, k_hs, v_ts, v_hs, q_ts, q_hs;
   uint16_t* q_out;
   const float *q_norm, *k_norm;
   const double* freq;
@@ -92,6 +92,11 @@ __device__ __forceinline__ float sigmoid(float x) {
 // tokens of sequence b in the cache, the new ones included
 __device__ __forceinline__ int seq_length(const int32_t* length, int b, int max_pages, int page_log) {
   return min(max(length[b], 0), max_pages << page_log);
+}
+
+// First element of head h's row of token t.
+__device__ __forceinline__ int64_t row_at(int t, int32_t ts, int h, int32_t hs) {
+  return static_cast<int64_t>(t) * ts + static_cast<int64_t>(h) * hs;
 }
 
 // Rows [begin, end) of sequence b, with the offsets forced into [0, N].

@@ -55,11 +55,11 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
     const size_t at = (((static_cast<size_t>(page) * a.Hk + (h < a.Hk ? h : h - a.Hk)) << a.page_log) + slot) * D + c0;
     dst = (h < a.Hk ? a.kc : a.vc) + at;
     if (h >= a.Hk) {
-      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(a.v + t * a.v_ts + (h - a.Hk) * a.v_hs + c0);
+      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(a.v + row_at(t, a.v_ts, h - a.Hk, a.v_hs) + c0);
       return;
     }
   }
-  const uint16_t* src = row < nq ? a.q + t * a.q_ts + row * a.q_hs : a.k + t * a.k_ts + h * a.k_hs;
+  const uint16_t* src = row < nq ? a.q + row_at(t, a.q_ts, row, a.q_hs) : a.k + row_at(t, a.k_ts, h, a.k_hs);
   const float* norm = row < nq ? a.q_norm : a.k_norm;
   if (!norm && c0 >= a.rot) {
     *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src + c0);

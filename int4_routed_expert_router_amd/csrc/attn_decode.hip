@@ -218,7 +218,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_decode(AttnArgs a, uint8_t* ws)
     for (int i = 0; i < W::kBlocks; ++i)
 #pragma unroll
       for (int j = 0; j < W::kVec; ++j) s.o[i][j] = f32x4_t{0, 0, 0, 0};
-    const uint16_t* qp = a.q + b * a.q_ts + (h * group + min(n16, group - 1)) * a.q_hs + 8 * quad;
+    const uint16_t* qp = a.q + row_at(b, a.q_ts, h * group + min(n16, group - 1), a.q_hs) + 8 * quad;
 #pragma unroll
     for (int i = 0; i < W::kSteps; ++i) s.q[i] = *reinterpret_cast<const uint4*>(qp + 32 * i);
 
@@ -301,9 +301,9 @@ __global__ __launch_bounds__(256, 2) void k_attn_decode(AttnArgs a, uint8_t* ws)
       if (whole) {
         const float inv = lsum != 0 ? 1.0f / lsum : 0.0f;
         x *= inv;
-        const size_t hq = h * group + row;
+        const int hq = h * group + row;
         if (a.gate) {
-          const uint2 g = *reinterpret_cast<const uint2*>(a.gate + b * a.g_ts + hq * a.g_hs + d);
+          const uint2 g = *reinterpret_cast<const uint2*>(a.gate + row_at(b, a.g_ts, hq, a.g_hs) + d);
           x[0] *= sigmoid(act_to_f32<ACT>(g.x & 0xFFFFu)), x[1] *= sigmoid(act_to_f32<ACT>(g.x >> 16));
           x[2] *= sigmoid(act_to_f32<ACT>(g.y & 0xFFFFu)), x[3] *= sigmoid(act_to_f32<ACT>(g.y >> 16));
         }
@@ -395,9 +395,9 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, const uint8_t* ws) {
       }
       if (tid % lanes == 0 && piece < to) {
         x *= l != 0 ? 1.0f / l : 0.0f;
-        const size_t hq = h * group + row;
+        const int hq = h * group + row;
         if (a.gate) {
-          const uint2 g = *reinterpret_cast<const uint2*>(a.gate + b * a.g_ts + hq * a.g_hs + d);
+          const uint2 g = *reinterpret_cast<const uint2*>(a.gate + row_at(b, a.g_ts, hq, a.g_hs) + d);
           x[0] *= sigmoid(act_to_f32<ACT>(g.x & 0xFFFFu)), x[1] *= sigmoid(act_to_f32<ACT>(g.x >> 16));
           x[2] *= sigmoid(act_to_f32<ACT>(g.y & 0xFFFFu)), x[3] *= sigmoid(act_to_f32<ACT>(g.y >> 16));
         }

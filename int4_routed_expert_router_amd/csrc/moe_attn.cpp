@@ -54,8 +54,8 @@ moe_status check_rows(const char* name, const moe_attn_rows* r) {
   if (!r || !r->data || !at_aligned(r->data, 16))
     return set_error(MOE_EINVAL, "%s must be rows at a 16-byte aligned device pointer", name);
   for (const int64_t st : {r->token_stride, r->head_stride})
-    if (st < 0 || st % 8 || st > (1ll << 36))
-      return set_error(MOE_ESHAPE, "%s: a stride of %lld is not a multiple of 8 in [0, 2^36]", name,
+    if (st < 0 || st % 8 || st >= (1ll << 31))
+      return set_error(MOE_ESHAPE, "%s: a stride of %lld is not a multiple of 8 in [0, 2^31)", name,
                        static_cast<long long>(st));
   return MOE_OK;
 }
@@ -76,8 +76,10 @@ moe_status attend(const moe_attn_desc* d, const moe_kv_cache* c, const int32_t* 
   const size_t need = decode ? attn_decode_bytes(d) : attn_prefill_bytes(d, n);
   if (!ws || !at_aligned(ws, 256)) return set_error(MOE_EINVAL, "workspace must be a 256-byte aligned device pointer");
   if (ws_bytes < need) return set_error(MOE_EWORKSPACE, "workspace of %zu bytes < required %zu", ws_bytes, need);
+  auto i32 = [](int64_t v) { return static_cast<int32_t>(v); };
   AttnArgs a{u16(c->k), u16(c->v), c->table, c->length, off, u16(q->data), gate ? u16(gate->data) : nullptr,
-             q->token_stride, q->head_stride, gate ? gate->token_stride : 0, gate ? gate->head_stride : 0,
+             i32(q->token_stride), i32(q->head_stride), i32(gate ? gate->token_stride : 0),
+             i32(gate ? gate->head_stride : 0),
              static_cast<uint16_t*>(o), scale, d->batch, n, d->q_heads, d->kv_heads, log2_of(d->page_size),
              d->n_pages, d->max_pages};
   const hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -117,9 +119,11 @@ extern "C" moe_status moe_kv_append(const moe_attn_desc* d, const moe_kv_cache* 
     return set_error(MOE_EINVAL, "eps must be finite and not negative");
   if (rot_dim && (!freq || !at_aligned(freq, 8)))
     return set_error(MOE_EINVAL, "rot_dim=%d needs freq, an 8-byte aligned device pointer", rot_dim);
+  auto i32 = [](int64_t v) { return static_cast<int32_t>(v); };
   moe::AppendArgs a{static_cast<uint16_t*>(c->k), static_cast<uint16_t*>(c->v), c->table, c->length, seq_off,
-                    moe::u16(k->data), moe::u16(v->data), q ? moe::u16(q->data) : nullptr, k->token_stride,
-                    k->head_stride, v->token_stride, v->head_stride, q ? q->token_stride : 0, q ? q->head_stride : 0,
+                    moe::u16(k->data), moe::u16(v->data), q ? moe::u16(q->data) : nullptr, i32(k->token_stride),
+                    i32(k->head_stride), i32(v->token_stride), i32(v->head_stride), i32(q ? q->token_stride : 0),
+                    i32(q ? q->head_stride : 0),
                     static_cast<uint16_t*>(q_out), q_norm, k_norm, freq, eps, rot_dim, d->batch, n_tokens, d->q_heads,
                     d->kv_heads, moe::log2_of(d->page_size), d->n_pages, d->max_pages};
   const hipError_t e =
