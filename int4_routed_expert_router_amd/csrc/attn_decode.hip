@@ -62,7 +62,7 @@ __device__ __forceinline__ uint32_t run_of_tile(uint32_t t, uint32_t per, uint32
   return t < big ? t / (per + 1) : more + (t - big) / per;
 }
 
-// The largest of a wave's lanes: sequences [64 c, 64 c + 64), this lane's length (0 behind the batch).
+// Sequences [64 c, 64 c + 64): this lane's length (0 behind the batch).
 __device__ __forceinline__ int chunk_length(const AttnArgs& a, int c) {
   const int b = 64 * c + (threadIdx.x & 63);
   return b < a.B ? seq_length(a.length, b, a.max_pages, a.page_log) : 0;
@@ -76,20 +76,21 @@ struct Wave {
   f32x4_t o[kBlocks][kVec];
   float m, l;
 
-  __device__ __forceinline__ void load_keys(const uint16_t* const (&at)[2], uint32_t el) {
+  // at: of each group of 16 keys, uniform; el: the lane's byte in it
+  __device__ __forceinline__ void load_keys(const uint8_t* const (&at)[2], uint32_t el) {
 #pragma unroll
     for (int g = 0; g < 2; ++g)
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) k[g][s] = *reinterpret_cast<const uint4*>(at[g] + el + 32 * s);
+      for (int s = 0; s < kSteps; ++s) k[g][s] = *reinterpret_cast<const uint4*>(at[g] + el + 64 * s);
   }
-  __device__ __forceinline__ void load_values(const uint16_t* const (&at)[2], uint32_t el) {
+  __device__ __forceinline__ void load_values(const uint8_t* const (&at)[2], uint32_t el) {
 #pragma unroll
     for (int g = 0; g < 2; ++g)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int n = 0; n < kBlocks; ++n) {
-          const uint16_t* p = at[g] + el + i * D + 128 * n;
+          const uint8_t* p = at[g] + el + (2 * i * D + 256 * n);
           if constexpr (kVec == 8) {
             const uint4 w = *reinterpret_cast<const uint4*>(p);
             v[g][i][n][0] = w.x, v[g][i][n][1] = w.y, v[g][i][n][2] = w.z, v[g][i][n][3] = w.w;
@@ -229,10 +230,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_decode(AttnArgs a, uint8_t* ws)
       const int id = pos < length ? table[pos >> a.page_log] : -1;
       pages = id < a.n_pages ? id : -1;
     };
-    auto group_at = [&](int t, int g, int& n) -> size_t {   // first element of a group and its keys
+    auto group_at = [&](int t, int g, int& n) -> size_t {   // first byte of a group, and its keys
       const int pos = t * kTile + 32 * wave + 16 * g, id = __builtin_amdgcn_readlane(pages, 2 * ((t - t0) & 31) + g);
       n = id < 0 ? 0 : min(16, length - pos);
-      return (((static_cast<size_t>(max(id, 0)) * a.Hk + h) << a.page_log) + (pos & ((1 << a.page_log) - 1))) * D;
+      return (((static_cast<size_t>(max(id, 0)) * a.Hk + h) << a.page_log) + (pos & ((1 << a.page_log) - 1))) * (2 * D);
     };
     load_pages(t0);
     int n[2], n_next[2];
@@ -242,21 +243,24 @@ __global__ __launch_bounds__(256, 2) void k_attn_decode(AttnArgs a, uint8_t* ws)
 #pragma unroll
       for (int g = 0; g < 2; ++g) el[g] = group_at(t, g, cnt[g]);
     };
-    const uint32_t k_el = n16 * D + 8 * quad, v_el = 4 * quad * D + W::kVec * n16;
+    const uint8_t *kc = reinterpret_cast<const uint8_t*>(a.k), *vc = reinterpret_cast<const uint8_t*>(a.v);
+    const uint32_t k_el = 2 * (n16 * D + 8 * quad), v_el = 2 * (4 * quad * D + W::kVec * n16);
     place(t0, n, e);
     {
-      const uint16_t* const kp[2] = {a.k + e[0], a.k + e[1]};
+      const uint8_t* const kp[2] = {kc + e[0], kc + e[1]};
       s.load_keys(kp, k_el);
     }
     for (int t = t0; t < t1; ++t) {
-      const uint16_t* const vp[2] = {a.v + e[0], a.v + e[1]};
+      const uint8_t* const vp[2] = {vc + e[0], vc + e[1]};
       s.load_values(vp, v_el);
+      __builtin_amdgcn_sched_barrier(0);   // all of them on their way before the keys are waited for
       f32x4_t z[2];
       s.scores(c, z);
       if (t + 1 < t1) {
         place(t + 1, n_next, e);
-        const uint16_t* const kp[2] = {a.k + e[0], a.k + e[1]};
+        const uint8_t* const kp[2] = {kc + e[0], kc + e[1]};
         s.load_keys(kp, k_el);
+        __builtin_amdgcn_sched_barrier(0);
       }
       if (min(n[0], n[1]) < 16) s.mask(n, z);
       uint4 hi, lo;
