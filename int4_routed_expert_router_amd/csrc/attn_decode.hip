@@ -29,7 +29,7 @@ namespace moe {
 namespace {
 
 constexpr int kTileLog = 7, kTile = 1 << kTileLog;   // keys of a tile
-constexpr int kMaxGroups = 512;                      // two workgroups on each of 256 compute units
+constexpr int kChip = 256;                           // compute units
 
 struct Part {   // an unfinished run: unit b * Hk + h (-1: none) and the workgroups that hold its parts
   int32_t unit, first, last, pad;
@@ -38,8 +38,9 @@ __host__ __device__ constexpr size_t ml_offset(int groups) { return sizeof(Part)
 __host__ __device__ constexpr size_t part_offset(int groups) { return ml_offset(groups) + sizeof(float2) * 2 * 16 * groups; }
 
 int groups_of(int64_t batch, int kv_heads, int64_t capacity) {
-  const int64_t tiles = batch * kv_heads * ((capacity + kTile - 1) >> kTileLog);
-  return static_cast<int>(tiles < kMaxGroups ? tiles : kMaxGroups);
+  const int64_t units = batch * kv_heads, tiles = units * ((capacity + kTile - 1) >> kTileLog);
+  const int most = units > kChip ? 2 * kChip : kChip;
+  return static_cast<int>(tiles < most ? tiles : most);
 }
 
 // Sum over the lanes up to this one.
@@ -68,6 +69,13 @@ __device__ __forceinline__ int chunk_length(const AttnArgs& a, int c) {
   return b < a.B ? seq_length(a.length, b, a.max_pages, a.page_log) : 0;
 }
 
+// Keys and values are read once a step: they are not to push out of the caches what is read again.
+template <class T>
+__device__ __forceinline__ T load_once(const uint8_t* p) {
+  typedef uint32_t words __attribute__((ext_vector_type(sizeof(T) / 4)));
+  return __builtin_bit_cast(T, __builtin_nontemporal_load(reinterpret_cast<const words*>(p)));
+}
+
 template <int ACT, int D>
 struct Wave {
   static constexpr int kSteps = D / 32, kVec = D >= 128 ? 8 : 4, kBlocks = D / (16 * kVec);
@@ -81,7 +89,7 @@ struct Wave {
 #pragma unroll
     for (int g = 0; g < 2; ++g)
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) k[g][s] = *reinterpret_cast<const uint4*>(at[g] + el + 64 * s);
+      for (int s = 0; s < kSteps; ++s) k[g][s] = load_once<uint4>(at[g] + el + 64 * s);
   }
   __device__ __forceinline__ void load_values(const uint8_t* const (&at)[2], uint32_t el) {
 #pragma unroll
@@ -92,10 +100,10 @@ struct Wave {
         for (int n = 0; n < kBlocks; ++n) {
           const uint8_t* p = at[g] + el + (2 * i * D + 256 * n);
           if constexpr (kVec == 8) {
-            const uint4 w = *reinterpret_cast<const uint4*>(p);
+            const uint4 w = load_once<uint4>(p);
             v[g][i][n][0] = w.x, v[g][i][n][1] = w.y, v[g][i][n][2] = w.z, v[g][i][n][3] = w.w;
           } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(p);
+            const uint2 w = load_once<uint2>(p);
             v[g][i][n][0] = w.x, v[g][i][n][1] = w.y;
           }
         }
