@@ -37,9 +37,9 @@ struct Part {   // an unfinished run: unit b * Hk + h (-1: none) and the workgro
 __host__ __device__ constexpr size_t ml_offset(int groups) { return sizeof(Part) * 2 * groups; }
 __host__ __device__ constexpr size_t part_offset(int groups) { return ml_offset(groups) + sizeof(float2) * 2 * 16 * groups; }
 
-int groups_of(int64_t batch, int kv_heads, int64_t capacity) {
+int groups_of(int64_t batch, int kv_heads, int64_t capacity, int head_dim) {
   const int64_t units = batch * kv_heads, tiles = units * ((capacity + kTile - 1) >> kTileLog);
-  const int most = units > kChip ? 2 * kChip : kChip;
+  const int most = head_dim < 256 && units > kChip ? 2 * kChip : kChip;
   return static_cast<int>(tiles < most ? tiles : most);
 }
 
@@ -54,11 +54,15 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t tiles_of(int len) { return static_cast<uint32_t>(len + kTile - 1) >> kTileLog; }
+__device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) >> kTileLog; }
+// A unit (a sequence's key head) costs two for each tile and one for its begin
+// and end (2 to 3 us, a tile takes 5); tiles that lie before position v of that.
+__device__ __forceinline__ uint32_t cost_of(int len) { return len > 0 ? 2 * tiles_of(len) + 1 : 0; }
+__device__ __forceinline__ int tile_at(uint32_t v, int n_tiles) { return min(static_cast<int>(v >> 1), n_tiles); }
 
-// Run of tiles of workgroup w, total tiles shared by n: the first total % n take one more.
+// Run of workgroup w of the whole cost: the first `more` are one longer than `per`.
 __device__ __forceinline__ uint32_t run_start(uint32_t w, uint32_t per, uint32_t more) { return w * per + min(w, more); }
-__device__ __forceinline__ uint32_t run_of_tile(uint32_t t, uint32_t per, uint32_t more) {
+__device__ __forceinline__ uint32_t run_of(uint32_t t, uint32_t per, uint32_t more) {
   const uint32_t big = more * (per + 1);
   return t < big ? t / (per + 1) : more + (t - big) / per;
 }
@@ -181,7 +185,7 @@ struct Wave {
 };
 
 template <int ACT, int D>
-__global__ __launch_bounds__(256, 2) void k_attn_decode(AttnArgs a, uint8_t* ws) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_decode(AttnArgs a, uint8_t* ws) {
   using W = Wave<ACT, D>;
   __shared__ float sm[4][16], sl[4][16];
   __shared__ __align__(16) float so[4][16][D];
@@ -196,85 +200,126 @@ __global__ __launch_bounds__(256, 2) void k_attn_decode(AttnArgs a, uint8_t* ws)
   // this workgroup's run of tiles, and the sequence it begins in
   const int chunks = (a.B + 63) / 64;
   int chunk = 0, len = chunk_length(a, 0);
-  uint32_t scan = wave_scan(tiles_of(len)), before = 0;   // tiles of a key head: up to this lane's sequence; before the chunk
-  uint32_t seq_tiles = __builtin_amdgcn_readlane(scan, 63);
-  for (int c = 1; c < chunks; ++c) seq_tiles += __builtin_amdgcn_readlane(wave_scan(tiles_of(chunk_length(a, c))), 63);
-  const uint32_t total = seq_tiles * a.Hk, per = total / n_groups, more = total % n_groups;
-  uint32_t tile = run_start(w, per, more);
-  const uint32_t stop = run_start(w + 1, per, more);
-  if (tile == stop) return;
-  while ((before + __builtin_amdgcn_readlane(scan, 63)) * a.Hk <= tile) {
+  uint32_t scan = wave_scan(cost_of(len)), before = 0;   // cost of a key head: up to this lane's sequence; before the chunk
+  uint32_t seq_cost = __builtin_amdgcn_readlane(scan, 63);
+  for (int c = 1; c < chunks; ++c) seq_cost += __builtin_amdgcn_readlane(wave_scan(cost_of(chunk_length(a, c))), 63);
+  // runs of at least two, so that one that lies within a unit has a tile of it
+  const uint32_t total = seq_cost * a.Hk, runs = min(static_cast<uint32_t>(n_groups), max(total >> 1, 1u));
+  const uint32_t per = total / runs, more = total % runs;
+  if (w >= static_cast<int>(runs) || total == 0) return;
+  const uint32_t start = run_start(w, per, more), stop = run_start(w + 1, per, more);
+  while ((before + __builtin_amdgcn_readlane(scan, 63)) * a.Hk <= start) {
     before += __builtin_amdgcn_readlane(scan, 63);
     len = chunk_length(a, ++chunk);
-    scan = wave_scan(tiles_of(len));
+    scan = wave_scan(cost_of(len));
   }
-  int at = __builtin_ctzll(__ballot((before + scan) * a.Hk > tile));   // lane of the sequence
+  int at = __builtin_ctzll(__ballot((before + scan) * a.Hk > start));   // lane of the sequence
+
+  // A segment: the run's tiles [t0, t1) of one sequence and key head.
+  struct Segment {
+    int b, h, length, t0, t1, n_tiles;
+    uint32_t unit_start, unit_end, seq_end;
+  };
+  auto segment_at = [&](uint32_t v) {   // of the sequence in lane `at`
+    Segment g;
+    g.b = 64 * chunk + at, g.length = __builtin_amdgcn_readlane(len, at);
+    g.n_tiles = tiles_of(g.length);
+    const uint32_t cost = cost_of(g.length);
+    g.seq_end = (before + __builtin_amdgcn_readlane(scan, at)) * a.Hk;
+    const uint32_t seq_start = g.seq_end - cost * a.Hk;
+    g.h = (v - seq_start) / cost;
+    g.unit_start = seq_start + g.h * cost;
+    g.unit_end = g.unit_start + cost;
+    g.t0 = tile_at(v - g.unit_start, g.n_tiles);
+    g.t1 = tile_at(stop - g.unit_start, g.n_tiles);
+    return g;
+  };
+  auto segment_behind = [&](const Segment& g) {
+    if (g.unit_end == g.seq_end) {   // on to the next sequence that has tiles
+      uint64_t left = __ballot(len > 0) & (at == 63 ? 0ull : ~0ull << (at + 1));
+      while (left == 0) {
+        before += __builtin_amdgcn_readlane(scan, 63);
+        len = chunk_length(a, ++chunk);
+        scan = wave_scan(cost_of(len));
+        left = __ballot(len > 0);
+      }
+      at = __builtin_ctzll(left);
+    }
+    return segment_at(g.unit_end);
+  };
 
   const float c = a.scale * kLog2e;
-  while (tile < stop) {
-    // sequence, key head and the run's tiles of it
-    const int b = 64 * chunk + at, length = __builtin_amdgcn_readlane(len, at);
-    const uint32_t n_tiles = tiles_of(length);
-    const uint32_t seq_start = (before + __builtin_amdgcn_readlane(scan, at) - n_tiles) * a.Hk;
-    const int h = (tile - seq_start) / n_tiles;
-    const uint32_t unit_start = seq_start + h * n_tiles;
-    const int t0 = tile - unit_start, t1 = min(n_tiles, stop - unit_start);
-    const int32_t* table = a.table + static_cast<size_t>(b) * a.max_pages;
-
-    W s;
+  const uint8_t *kc = reinterpret_cast<const uint8_t*>(a.k), *vc = reinterpret_cast<const uint8_t*>(a.v);
+  const uint32_t k_el = 2 * (n16 * D + 8 * quad), v_el = 2 * (4 * quad * D + W::kVec * n16);
+  W s;
+  Segment cur = segment_at(start);
+  auto is_last = [&](const Segment& g) { return stop <= g.unit_end + 1; };   // of the next unit at most the begin
+  if (cur.t0 == cur.t1) {   // all tiles of the unit lie before
+    if (is_last(cur)) return;
+    cur = segment_behind(cur);
+  }
+  // Pages of this wave's groups of 16 keys, two a tile, 32 tiles at a time: one to a lane (-1: none).
+  int pages = -1, n[2], n_next[2];   // keys of a tile's two groups
+  size_t e[2];                       // their first bytes
+  auto load_pages = [&](const Segment& g, int t) {
+    const int pos = (t + (lane >> 1)) * kTile + 32 * wave + 16 * (lane & 1);
+    const int id = pos < g.length ? a.table[static_cast<size_t>(g.b) * a.max_pages + (pos >> a.page_log)] : -1;
+    pages = id < a.n_pages ? id : -1;
+  };
+  auto place = [&](const Segment& g, int t) {
+    if (t > g.t0 && ((t - g.t0) & 31) == 0) load_pages(g, t);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int pos = t * kTile + 32 * wave + 16 * i, id = __builtin_amdgcn_readlane(pages, 2 * ((t - g.t0) & 31) + i);
+      n_next[i] = id < 0 ? 0 : min(16, g.length - pos);
+      e[i] = (((static_cast<size_t>(max(id, 0)) * a.Hk + g.h) << a.page_log) + (pos & ((1 << a.page_log) - 1))) * (2 * D);
+    }
+  };
+  auto load_keys = [&]() {
+    const uint8_t* const kp[2] = {kc + e[0], kc + e[1]};
+    s.load_keys(kp, k_el);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto begin = [&](const Segment& g) {   // its pages, queries and first keys
+    load_pages(g, g.t0);
+    const uint16_t* qp = a.q + row_at(g.b, a.q_ts, g.h * group + min(n16, group - 1), a.q_hs) + 8 * quad;
+#pragma unroll
+    for (int i = 0; i < W::kSteps; ++i) s.q[i] = *reinterpret_cast<const uint4*>(qp + 32 * i);
+    place(g, g.t0);
+    load_keys();
+  };
+  begin(cur);
+  for (;;) {
     s.m = -INFINITY, s.l = 0;
 #pragma unroll
     for (int i = 0; i < W::kBlocks; ++i)
 #pragma unroll
       for (int j = 0; j < W::kVec; ++j) s.o[i][j] = f32x4_t{0, 0, 0, 0};
-    const uint16_t* qp = a.q + row_at(b, a.q_ts, h * group + min(n16, group - 1), a.q_hs) + 8 * quad;
+    const bool whole = cur.t0 == 0 && cur.t1 == cur.n_tiles, last = is_last(cur);
+    constexpr int kPieces = 16 * D / 1024;   // of four outputs, most that a thread has
+    uint2 gates[kPieces];
+    if (whole && a.gate) {
 #pragma unroll
-    for (int i = 0; i < W::kSteps; ++i) s.q[i] = *reinterpret_cast<const uint4*>(qp + 32 * i);
-
-    // Pages of this wave's groups of 16 keys, two a tile, 32 tiles at a time: one to a lane (-1: none).
-    int pages = -1;
-    auto load_pages = [&](int t) {
-      const int pos = (t + (lane >> 1)) * kTile + 32 * wave + 16 * (lane & 1);
-      const int id = pos < length ? table[pos >> a.page_log] : -1;
-      pages = id < a.n_pages ? id : -1;
-    };
-    auto group_at = [&](int t, int g, int& n) -> size_t {   // first byte of a group, and its keys
-      const int pos = t * kTile + 32 * wave + 16 * g, id = __builtin_amdgcn_readlane(pages, 2 * ((t - t0) & 31) + g);
-      n = id < 0 ? 0 : min(16, length - pos);
-      return (((static_cast<size_t>(max(id, 0)) * a.Hk + h) << a.page_log) + (pos & ((1 << a.page_log) - 1))) * (2 * D);
-    };
-    load_pages(t0);
-    int n[2], n_next[2];
-    size_t e[2];
-    auto place = [&](int t, int (&cnt)[2], size_t (&el)[2]) {
-      if (t > t0 && ((t - t0) & 31) == 0) load_pages(t);
-#pragma unroll
-      for (int g = 0; g < 2; ++g) el[g] = group_at(t, g, cnt[g]);
-    };
-    const uint8_t *kc = reinterpret_cast<const uint8_t*>(a.k), *vc = reinterpret_cast<const uint8_t*>(a.v);
-    const uint32_t k_el = 2 * (n16 * D + 8 * quad), v_el = 2 * (4 * quad * D + W::kVec * n16);
-    place(t0, n, e);
-    {
-      const uint8_t* const kp[2] = {kc + e[0], kc + e[1]};
-      s.load_keys(kp, k_el);
+      for (int i = 0; i < kPieces; ++i) {
+        const int x = 4 * threadIdx.x + 1024 * i, row = x / D;
+        if (row < group) gates[i] = *reinterpret_cast<const uint2*>(a.gate + row_at(cur.b, a.g_ts, cur.h * group + row, a.g_hs) + x % D);
+      }
     }
-    for (int t = t0; t < t1; ++t) {
+    for (int t = cur.t0; t < cur.t1; ++t) {
+      n[0] = n_next[0], n[1] = n_next[1];
       const uint8_t* const vp[2] = {vc + e[0], vc + e[1]};
       s.load_values(vp, v_el);
       __builtin_amdgcn_sched_barrier(0);   // all of them on their way before the keys are waited for
       f32x4_t z[2];
       s.scores(c, z);
-      if (t + 1 < t1) {
-        place(t + 1, n_next, e);
-        const uint8_t* const kp[2] = {kc + e[0], kc + e[1]};
-        s.load_keys(kp, k_el);
-        __builtin_amdgcn_sched_barrier(0);
+      if (t + 1 < cur.t1) {
+        place(cur, t + 1);
+        load_keys();
       }
       if (min(n[0], n[1]) < 16) s.mask(n, z);
       uint4 hi, lo;
       s.softmax(z, hi, lo);
       s.add_values(hi, lo);
-      n[0] = n_next[0], n[1] = n_next[1];
     }
 
     // the four waves' results together
@@ -296,10 +341,11 @@ __global__ __launch_bounds__(256, 2) void k_attn_decode(AttnArgs a, uint8_t* ws)
                 make_float4(s.o[i][j][r] * f, s.o[i][j + 1][r] * f, s.o[i][j + 2][r] * f, s.o[i][j + 3][r] * f);
     }
     __syncthreads();
-    const bool whole = t0 == 0 && t1 == static_cast<int>(n_tiles);
-    const int slot = t0 > 0 ? 0 : 1;
-    for (int i = 4 * threadIdx.x; i < group * D; i += 1024) {
-      const int row = i / D, d = i % D;
+    const int slot = cur.t0 > 0 ? 0 : 1;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int at4 = 4 * threadIdx.x + 1024 * i, row = at4 / D, d = at4 % D;
+      if (row >= group) break;
       float mx = -INFINITY, lsum = 0;
 #pragma unroll
       for (int u = 0; u < 4; ++u) mx = fmaxf(mx, sm[u][row]);
@@ -311,38 +357,21 @@ __global__ __launch_bounds__(256, 2) void k_attn_decode(AttnArgs a, uint8_t* ws)
         x += *reinterpret_cast<const f32x4_t*>(&so[u][row][d]);
       }
       if (whole) {
-        const float inv = lsum != 0 ? 1.0f / lsum : 0.0f;
-        x *= inv;
-        const int hq = h * group + row;
-        if (a.gate) {
-          const uint2 g = *reinterpret_cast<const uint2*>(a.gate + row_at(b, a.g_ts, hq, a.g_hs) + d);
-          x[0] *= sigmoid(act_to_f32<ACT>(g.x & 0xFFFFu)), x[1] *= sigmoid(act_to_f32<ACT>(g.x >> 16));
-          x[2] *= sigmoid(act_to_f32<ACT>(g.y & 0xFFFFu)), x[3] *= sigmoid(act_to_f32<ACT>(g.y >> 16));
-        }
-        *reinterpret_cast<uint2*>(a.o + (static_cast<size_t>(b) * a.Hq + hq) * D + d) =
-            make_uint2(pack2<ACT>(x[0], x[1]), pack2<ACT>(x[2], x[3]));
+        x *= lsum != 0 ? 1.0f / lsum : 0.0f;
+        store_row<ACT>(a, cur.b, cur.h * group + row, D, d, x, gates[i]);
       } else {
         *reinterpret_cast<f32x4_t*>(part_o + (slot * 16 + row) * D + d) = x;
         if (d == 0) part_ml[slot * 16 + row] = make_float2(mx, lsum);
       }
     }
     if (!whole && threadIdx.x == 0) {
-      const uint32_t last = unit_start + n_tiles - 1;
-      parts[slot] = Part{b * a.Hk + h, static_cast<int>(run_of_tile(unit_start, per, more)),
-                         static_cast<int>(run_of_tile(last, per, more)), 0};
+      parts[slot] = Part{cur.b * a.Hk + cur.h, static_cast<int>(run_of(cur.unit_start + 1, per, more)),
+                         static_cast<int>(run_of(cur.unit_end - 2, per, more)), 0};   // the runs that hold a tile of it
     }
+    if (last) return;
+    cur = segment_behind(cur);
+    begin(cur);
     __syncthreads();   // sm, sl and so are free again
-    tile = unit_start + t1;
-    if (tile < stop && tile == seq_start + n_tiles * a.Hk) {   // on to the next sequence that has tiles
-      uint64_t left = __ballot(len > 0) & (at == 63 ? 0ull : ~0ull << (at + 1));
-      while (left == 0) {
-        before += __builtin_amdgcn_readlane(scan, 63);
-        len = chunk_length(a, ++chunk);
-        scan = wave_scan(tiles_of(len));
-        left = __ballot(len > 0);
-      }
-      at = __builtin_ctzll(left);
-    }
   }
 }
 
@@ -407,14 +436,7 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, const uint8_t* ws) {
       }
       if (tid % lanes == 0 && piece < to) {
         x *= l != 0 ? 1.0f / l : 0.0f;
-        const int hq = h * group + row;
-        if (a.gate) {
-          const uint2 g = *reinterpret_cast<const uint2*>(a.gate + row_at(b, a.g_ts, hq, a.g_hs) + d);
-          x[0] *= sigmoid(act_to_f32<ACT>(g.x & 0xFFFFu)), x[1] *= sigmoid(act_to_f32<ACT>(g.x >> 16));
-          x[2] *= sigmoid(act_to_f32<ACT>(g.y & 0xFFFFu)), x[3] *= sigmoid(act_to_f32<ACT>(g.y >> 16));
-        }
-        *reinterpret_cast<uint2*>(a.o + (static_cast<size_t>(b) * a.Hq + hq) * D + d) =
-            make_uint2(pack2<ACT>(x[0], x[1]), pack2<ACT>(x[2], x[3]));
+        store_row<ACT>(a, b, h * group + row, D, d, x, gates_of(a, b, h * group + row, d));
       }
       __syncthreads();
     }
@@ -427,7 +449,7 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, const uint8_t* ws) {
 
 template <int ACT, int D>
 hipError_t launch(const AttnArgs& a, void* ws, hipStream_t s) {
-  const int groups = groups_of(a.B, a.Hk, static_cast<int64_t>(a.max_pages) << a.page_log);
+  const int groups = groups_of(a.B, a.Hk, static_cast<int64_t>(a.max_pages) << a.page_log, D);
   hipLaunchKernelGGL((k_attn_decode<ACT, D>), dim3(groups), dim3(256), 0, s, a, static_cast<uint8_t*>(ws));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -438,7 +460,7 @@ hipError_t launch(const AttnArgs& a, void* ws, hipStream_t s) {
 }  // namespace
 
 size_t attn_decode_bytes(const moe_attn_desc* d) {
-  const int groups = groups_of(d->batch, d->kv_heads, static_cast<int64_t>(d->max_pages) * d->page_size);
+  const int groups = groups_of(d->batch, d->kv_heads, static_cast<int64_t>(d->max_pages) * d->page_size, d->head_dim);
   return part_offset(groups) + sizeof(float) * 2 * 16 * d->head_dim * groups;
 }
 

@@ -260,20 +260,6 @@ __device__ __forceinline__ uint2 read_transposed(const uint8_t* p) {
                                        (__attribute__((address_space(3))) s16x4_t*)(p)));
 }
 
-// Four neighbouring normalised values of a row with their gates, if there are any.
-template <int ACT, int D>
-__device__ __forceinline__ void store_row(const AttnArgs& a, int t, int hq, int d, f32x4_t v, uint2 g) {
-  if (a.gate) {
-    v[0] *= sigmoid(act_to_f32<ACT>(g.x & 0xFFFFu)), v[1] *= sigmoid(act_to_f32<ACT>(g.x >> 16));
-    v[2] *= sigmoid(act_to_f32<ACT>(g.y & 0xFFFFu)), v[3] *= sigmoid(act_to_f32<ACT>(g.y >> 16));
-  }
-  *reinterpret_cast<uint2*>(a.o + (static_cast<int64_t>(t) * a.Hq + hq) * D + d) =
-      make_uint2(pack2<ACT>(v[0], v[1]), pack2<ACT>(v[2], v[3]));
-}
-__device__ __forceinline__ uint2 gates_of(const AttnArgs& a, int t, int hq, int d) {
-  return a.gate ? *reinterpret_cast<const uint2*>(a.gate + row_at(t, a.g_ts, hq, a.g_hs) + d) : make_uint2(0, 0);
-}
-
 template <int ACT, class S>
 __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint8_t* ws) {
   constexpr int D = S::D, kT = S::kT, kW = S::kW, kTileBytes = kKeys * D * 2;
@@ -601,7 +587,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
               }
 #pragma unroll
               for (int e = 0; e < kBatch; ++e)
-                if (w[e].real) store_row<ACT, D>(a, u.begin + tok0 + w[e].tok, w[e].head, d, x[e], g[e]);
+                if (w[e].real) store_row<ACT>(a, u.begin + tok0 + w[e].tok, w[e].head, D, d, x[e], g[e]);
             } else {
 #pragma unroll
               for (int e = 0; e < kBatch; ++e)
@@ -683,7 +669,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, const uint8_t* ws
         if (tid % lanes == 0 && piece < to) {
           const int t = row / group;
           const int hq = u.h * group + row - t * group;
-          store_row<ACT, D>(a, u.begin + tok0 + t, hq, d, x * (l != 0 ? 1.0f / l : 0.0f),
+          store_row<ACT>(a, u.begin + tok0 + t, hq, D, d, x * (l != 0 ? 1.0f / l : 0.0f),
                             gates_of(a, u.begin + tok0 + t, hq, d));
         }
       }
