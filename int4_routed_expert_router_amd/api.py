@@ -568,7 +568,8 @@ class KVCache:
     [B, max_pages] int32, the pages of each sequence in order (an entry outside
     [0, n_pages): no page); length: [B] int32, each sequence's tokens, those of
     the call included.  All contiguous, on one GPU; table and length may change
-    between calls, also between replays of a captured one."""
+    between calls, also between replays of a captured one.  The object keeps the
+    tensors; other ones take another object."""
 
     def __init__(self, k, v, table, length):
         dev = _device(k, "k")
@@ -583,22 +584,24 @@ class KVCache:
         for t, name, dtypes in ((k, "k", (k.dtype,)), (v, "v", (k.dtype,)), (table, "table", _I32),
                                 (length, "length", _I32)):
             _arg(t, name, dtypes, None, dev)
-        self.k, self.v, self.table, self.length = k, v, table, length
         self.n_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.batch, self.max_pages = table.shape
-        self._dev = dev
-        self._desc = {}
+        self._tensors = (k, v, table, length)
+        self._dev, self._dtype, self._desc = dev, k.dtype, {}
+        self._c = KvCacheC(k.data_ptr(), v.data_ptr(), table.data_ptr(), length.data_ptr())
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    table = property(lambda self: self._tensors[2])
+    length = property(lambda self: self._tensors[3])
 
     def desc(self, q_heads):
         """The call's shape for q_heads query heads."""
         d = self._desc.get(q_heads)
         if d is None:
             d = self._desc[q_heads] = AttnDesc(self.batch, q_heads, self.kv_heads, self.head_dim,
-                                               _ACT_OF[self.k.dtype], self.page_size, self.n_pages, self.max_pages)
+                                               _ACT_OF[self._dtype], self.page_size, self.n_pages, self.max_pages)
         return d
-
-    def _c(self):
-        return KvCacheC(self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(), self.length.data_ptr())
 
     def _rows(self, t, name, shape=None):
         """Strided rows [T, heads, head_dim] for the C ABI."""
@@ -606,19 +609,20 @@ class KVCache:
             return None
         if _device(t, name) != self._dev:
             raise ValueError(f"{name} is on {t.device}, expected cuda:{self._dev}")
-        if t.dim() != 3 or t.shape[2] != self.head_dim or (shape is not None and t.shape != shape):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+        sh = t.shape
+        if len(sh) != 3 or sh[2] != self.head_dim or (shape is not None and sh != shape):
+            raise ValueError(f"{name} has shape {tuple(sh)}, expected "
                              f"{tuple(shape) if shape is not None else ('T', 'heads', self.head_dim)}")
-        if t.dtype != self.k.dtype:
-            raise ValueError(f"{name} has dtype {t.dtype}, expected {self.k.dtype}")
-        st, sh, sd = t.stride()
-        if sd != 1:
+        if t.dtype is not self._dtype:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {self._dtype}")
+        token, head, one = t.stride()
+        if one != 1:
             raise ValueError(f"{name}: the values of a head must lie next to each other")
         # the stride of a dimension of one is never used
-        return AttnRows(t.data_ptr(), st if t.shape[0] > 1 else 0, sh if t.shape[1] > 1 else 0)
+        return AttnRows(t.data_ptr(), token if sh[0] > 1 else 0, head if sh[1] > 1 else 0)
 
     def _out(self, t, name, shape):
-        p = _arg(t, name, (self.k.dtype,), None, self._dev)
+        p = _arg(t, name, (self._dtype,), None, self._dev)
         if p is None or t.shape != shape:
             raise ValueError(f"{name} must be a tensor of shape {tuple(shape)}")
         return p
@@ -647,7 +651,7 @@ def kv_append(cache, k, v, seq_off=None, q=None, q_out=None, q_norm=None, k_norm
     if q is None and q_out is not None:
         raise ValueError("q_out needs q")
     _call_on(dev, lib().moe_kv_append, C.byref(cache.desc(cache.kv_heads if q is None else q.shape[1])),
-             C.byref(cache._c()), _arg(seq_off, "seq_off", _I32, cache.batch + 1, dev), N, C.byref(kr), C.byref(vr),
+             C.byref(cache._c), _arg(seq_off, "seq_off", _I32, cache.batch + 1, dev), N, C.byref(kr), C.byref(vr),
              _ref(qr), None if q is None else cache._out(q_out, "q_out", q.shape),
              _arg(q_norm, "q_norm", _F32, D, dev), _arg(k_norm, "k_norm", _F32, D, dev), float(eps),
              _arg(freq, "freq", (torch.float64,), None, dev), 0 if freq is None else 2 * freq.numel(),
@@ -668,7 +672,7 @@ def _attend(cache, q, o, gate, ws, stream, decode):
     if ws is None:
         with _allocating_on(stream):
             ws = attn_workspace(cache, q.shape[1], None if decode else q.shape[0])
-    return (C.byref(cache.desc(q.shape[1])), C.byref(cache._c())), (C.byref(qr), _ref(gr)), (
+    return (C.byref(cache.desc(q.shape[1])), C.byref(cache._c)), (C.byref(qr), _ref(gr)), (
         op, _arg(ws, "ws", (torch.uint8,), None, cache._dev), ws.numel(), _stream_on(cache._dev, stream))
 
 
