@@ -449,6 +449,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
         // Operands are read kAhead products before they are used.
         const uint8_t* kp = &tiles[buf][0][(32 * sub + (ln & 31)) * D * 2];
         auto key_part = [&](int i) { return *reinterpret_cast<const uint4*>(kp + (((2 * i + hl) ^ (ln & 7)) << 4)); };
+        if constexpr (D > 64) __builtin_amdgcn_s_setprio(1);   // the wave in its products first
         uint4 kf[kAhead];
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) kf[i] = key_part(i);
@@ -465,6 +466,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
           __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
         }
         __builtin_amdgcn_sched_group_barrier(0x8, kT * kAhead, 0);
+        if constexpr (D > 64) __builtin_amdgcn_s_setprio(0);
         if (key0 + 31 > low || alive_now != 15) {
 #pragma unroll
           for (int r = 0; r < kT; ++r)
@@ -519,6 +521,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
           const uint2 x = read_transposed(vi), y = read_transposed(vi + 8 * D * 2);
           return make_uint4(x.x, x.y, y.x, y.y);
         };
+        if constexpr (D > 64) __builtin_amdgcn_s_setprio(1);
         uint4 vf[kAhead];
 #pragma unroll
         for (int n = 0; n < kAhead; ++n) vf[n] = value_part(n);
@@ -535,6 +538,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
           __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
         }
         __builtin_amdgcn_sched_group_barrier(0x8, kT * kAhead, 0);
+        if constexpr (D > 64) __builtin_amdgcn_s_setprio(0);
       }
     }
 
@@ -692,11 +696,13 @@ template <int ACT, int D>
 hipError_t launch(const AttnArgs& a, void* ws, hipStream_t s) {
   using S = Shape<D>;
   const int64_t units = units_of(a.N, a.B, a.Hq, a.Hk);
-  const int grid = static_cast<int>(units < S::kRuns ? S::kRuns : units);
+  // the runs that a cut call can have, eight or a multiple
+  const int64_t cost = units * ((static_cast<int64_t>(a.max_pages) << a.page_log) + kStart), most = ((cost >> kRunLog) / 8 + 1) * 8;
+  const int runs = static_cast<int>(most < S::kRuns ? most : S::kRuns), grid = static_cast<int>(units > runs ? units : runs);
   hipLaunchKernelGGL((k_attn_prefill<ACT, S>), dim3(grid), dim3(64 * S::kW), 0, s, a, static_cast<uint8_t*>(ws));
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((k_attn_join<ACT, S>), dim3(2 * S::kRuns, kSlices), dim3(256), 0, s, a,
+  hipLaunchKernelGGL((k_attn_join<ACT, S>), dim3(2 * runs, kSlices), dim3(256), 0, s, a,
                      static_cast<const uint8_t*>(ws));
   return hipGetLastError();
 }
