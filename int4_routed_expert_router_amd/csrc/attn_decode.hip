@@ -208,7 +208,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_decode(AttnArgs 
   const uint32_t per = total / runs, more = total % runs;
   if (w >= static_cast<int>(runs) || total == 0) return;
   const uint32_t start = run_start(w, per, more), stop = run_start(w + 1, per, more);
+  // (searches end with the batch also if lengths change under them)
   while ((before + __builtin_amdgcn_readlane(scan, 63)) * a.Hk <= start) {
+    if (chunk + 1 == chunks) return;
     before += __builtin_amdgcn_readlane(scan, 63);
     len = chunk_length(a, ++chunk);
     scan = wave_scan(cost_of(len));
@@ -238,6 +240,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_decode(AttnArgs 
     if (g.unit_end == g.seq_end) {   // on to the next sequence that has tiles
       uint64_t left = __ballot(len > 0) & (at == 63 ? 0ull : ~0ull << (at + 1));
       while (left == 0) {
+        if (chunk + 1 == chunks) return Segment{g.b, g.h, 0, 0, 0, 0, stop, stop, stop};
         before += __builtin_amdgcn_readlane(scan, 63);
         len = chunk_length(a, ++chunk);
         scan = wave_scan(cost_of(len));
@@ -257,6 +260,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_decode(AttnArgs 
   if (cur.t0 == cur.t1) {   // all tiles of the unit lie before
     if (is_last(cur)) return;
     cur = segment_behind(cur);
+    if (cur.t0 == cur.t1) return;
   }
   // Pages of this wave's groups of 16 keys, two a tile, 32 tiles at a time: one to a lane (-1: none).
   int pages = -1, n[2], n_next[2];   // keys of a tile's two groups
@@ -370,6 +374,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_decode(AttnArgs 
     }
     if (last) return;
     cur = segment_behind(cur);
+    if (cur.t0 == cur.t1) return;
     begin(cur);
     __syncthreads();   // sm, sl and so are free again
   }

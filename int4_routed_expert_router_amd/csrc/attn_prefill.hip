@@ -162,7 +162,7 @@ __device__ bool begin_work(const AttnArgs& a, int tpb, Unit& u, bool& cut, Runs&
   if (!cut) {
     if (blockIdx.x >= units) return false;
     int64_t items = 0;
-    for (int c = 0;; ++c) {
+    for (int c = 0; c < chunks; ++c) {
       if (chunks > 1) s.load(a, 64 * c + lane, tpb);
       const int64_t up = wave_scan64(s.blocks - s.first);
       const uint64_t hit = __ballot((items + up) * a.Hk > blockIdx.x);
@@ -177,8 +177,10 @@ __device__ bool begin_work(const AttnArgs& a, int tpb, Unit& u, bool& cut, Runs&
       }
       items += lane64(up, 63);
     }
+    return false;
   }
-  runs.n = static_cast<int>(min(static_cast<int64_t>(S::kRuns), (total >> kRunLog) + 1));
+  // (offsets in no order can name more work than the host counted: no more runs than workgroups)
+  runs.n = min(static_cast<int>(min(static_cast<int64_t>(S::kRuns), (total >> kRunLog) + 1)), static_cast<int>(gridDim.x) & ~7);
   runs.per = total / runs.n;
   runs.more = static_cast<int>(total - runs.per * runs.n);
   const int die_runs = (runs.n + 7) / 8;
@@ -186,7 +188,7 @@ __device__ bool begin_work(const AttnArgs& a, int tpb, Unit& u, bool& cut, Runs&
   if (static_cast<int>(blockIdx.x / 8) >= die_runs || run >= runs.n) return false;
   const int64_t pos = runs.start(run);
   int64_t sum = 0;
-  for (int c = 0;; ++c) {
+  for (int c = 0; c < chunks; ++c) {
     if (chunks > 1) {
       s.load(a, 64 * c + lane, tpb);
       upto = wave_scan64(s.all(tpb));
@@ -218,14 +220,15 @@ __device__ bool begin_work(const AttnArgs& a, int tpb, Unit& u, bool& cut, Runs&
     }
     sum += lane64(upto, 63);
   }
+  return false;
 }
 
-// The unit behind u in rising order (there is one).
-__device__ void next_unit(const AttnArgs& a, int tpb, Unit& u) {
-  if (++u.h < a.Hk) return;
+// The unit behind u in rising order (false: there is none).
+__device__ bool next_unit(const AttnArgs& a, int tpb, Unit& u) {
+  if (++u.h < a.Hk) return true;
   u.h = 0;
-  if (++u.j < u.blocks) return;
-  for (int b = u.b + 1;; b += 64) {
+  if (++u.j < u.blocks) return true;
+  for (int b = u.b + 1; b < a.B; b += 64) {
     Seq s;
     s.load(a, b + (threadIdx.x & 63), tpb);
     const uint64_t hit = __ballot(s.blocks > s.first);
@@ -234,9 +237,10 @@ __device__ void next_unit(const AttnArgs& a, int tpb, Unit& u) {
       const Seq q = s.of_lane(at);
       set_sequence(u, b + at, q);
       u.j = q.first;
-      return;
+      return true;
     }
   }
+  return false;
 }
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
@@ -614,7 +618,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
     }   // a run's part of a unit may be none of its tiles
     unit_start += pos0 + n_tok + kStart;
     if (!cut || unit_start >= runs.start(run + 1)) return;
-    next_unit(a, tpb, u);
+    if (!next_unit(a, tpb, u)) return;
     __syncthreads();   // the tiles' places are free again
   }
 }

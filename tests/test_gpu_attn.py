@@ -77,6 +77,35 @@ def test_prefill_of_many_sequences(B):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("shape,new,old", [
+    ((16, 2, 256, 64), [100 + i % 31 for i in range(40)], [0] * 40),        # more units than compute units, none cut
+    ((4, 2, 64, 16), [1 + i % 3 for i in range(100)], [3000 if i == 77 else i % 20 for i in range(100)]),
+    ((2, 1, 128, 32), [0] * 70 + [400], [9] * 70 + [1000]),                 # the only tokens come last
+    ((16, 1, 128, 128), [3, 1], [2500, 0]),
+    ((11, 1, 256, 16), [50], [77]), ((7, 1, 64, 16), [90, 1], [3, 500]), ((13, 1, 128, 64), [64], [0]),
+], ids=str)
+def test_prefill_of_uneven_batches(shape, new, old):
+    c = case(new, [a + b for a, b in zip(new, old)], *shape, "bf16", seed=len(new))
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_random_shapes(seed):
+    # any group up to 16, pages, lengths, both calls on the same cache
+    import random
+    r = random.Random(seed)
+    hk, d, page = r.choice((1, 1, 2, 3)), r.choice((64, 128, 256)), r.choice((16, 32, 64, 128, 256))
+    B = r.choice((1, 2, 5, 17, 70))
+    most = 1500 // B
+    new = [r.choice((0, 1, 1, 2, r.randint(0, 40), r.randint(0, most // 3 + 1))) for _ in range(B)]
+    old = [r.choice((0, 1, r.randint(0, most), r.randint(0, 2 * most))) for _ in range(B)]
+    c = case(new, [a + b for a, b in zip(new, old)], hk * r.randint(1, 16), hk, d, page, r.choice(("bf16", "f16")),
+             gate=r.random() < 0.5, seed=seed, spread=r.choice((0.3, 1.5, 4.0)))
+    c.check(c.run())
+    if c.q.shape[0] >= B:
+        c.check(c.run(decode=True), decode=True)
+
+
 # ------------------------------------------------------------------ what no token may see
 @pytest.mark.parametrize("decode", [True, False])
 def test_more_new_tokens_than_positions_and_lengths_out_of_range(decode):
@@ -294,6 +323,59 @@ def test_captured_calls_follow_the_lengths(decode):
         torch.cuda.synchronize()
         c.check(o, decode)
         assert torch.equal(o, c.run(decode))
+
+
+def test_two_graphs_that_share_a_workspace():
+    import torch
+    from int4_routed_expert_router_amd import api
+    a = case([1] * 4, [4000, 900, 0, 77], 16, 2, 256, 64, "bf16", seed=20)
+    b = case([500, 30], [900, 4000], 16, 2, 256, 64, "bf16", seed=21)
+    want = [a.run(True), b.run()]
+    ws = api.attn_workspace(b.cache(), 16, 600)
+    outs, graphs = [], []
+    for c, decode in ((a, True), (b, False)):
+        cache, n = c.cache(), len(c.new) if decode else c.q.shape[0]
+        o, q = torch.full(c.q[:n].shape, 7.0, dtype=c.q.dtype, device="cuda"), c.q[:n]
+
+        def call():
+            if decode:
+                api.attn_decode(cache, q, o, c.scale, ws=ws)
+            else:
+                api.attn_prefill(cache, q, o, c.off, c.scale, ws=ws)
+
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append((g, cache))
+        outs.append(o)
+    for _ in range(3):
+        for o in outs:
+            o.fill_(7.0)
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs, want))
+        a.run(True)
+        torch.cuda.synchronize()
+
+
+def test_offsets_in_no_order_stay_within_the_buffers():
+    # results are not defined, but every row outside the ranges keeps its values and nothing else is written
+    import torch
+    from int4_routed_expert_router_amd import api
+    c = case([30, 30, 30], [200, 300, 400], 4, 2, 64, 16, "bf16", seed=22)
+    n = c.q.shape[0]
+    for off in ([50, 10, 60, 20], [-7, 2 ** 31 - 1, -2 ** 31, 5], [92, 92, 0, 0], [0, 1000, 20, 90]):
+        c.off = torch.tensor(off, dtype=torch.int32).cuda()
+        pad = torch.full((n + 4, 4, 64), 7.0, dtype=c.q.dtype, device="cuda")
+        api.attn_prefill(c.cache(), c.q, pad[2 : n + 2], c.off, c.scale)
+        k, v = (torch.randn(n, 2, 64, device="cuda").to(c.q.dtype) for _ in range(2))
+        kc, vc = c.k.clone(), c.v.clone()
+        api.kv_append(api.KVCache(kc, vc, c.table, c.length), k, v, seq_off=c.off)
+        torch.cuda.synchronize()
+        assert (pad[:2] == 7).all() and (pad[n + 2 :] == 7).all()
 
 
 # ------------------------------------------------------------------ append
