@@ -626,7 +626,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
 // Adds up the parts of units that several runs hold: the workgroups of a unit's
 // runs share its outputs, four neighbouring ones to a piece, kSlices workgroups
 // to a part.  Also writes the zeros of rows that have no position.
-constexpr int kSlices = 4;
+constexpr int kSlices = 8;
 template <int ACT, class S>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, const uint8_t* ws) {
   constexpr int D = S::D;
