@@ -269,6 +269,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
   constexpr int D = S::D, kT = S::kT, kW = S::kW, kTileBytes = kKeys * D * 2;
   constexpr int kSteps = D / 16, kBlocks = D / 32, kAhead = S::kAhead, kPieces = D / 8;   // 16-byte pieces of a row
   constexpr int kLoadKeys = 64 / kPieces, kLoads = kKeys / (kLoadKeys * kW);
+  constexpr int kKeySwap = D == 64 ? 7 : 15;   // the pieces' order depends on the key: no bank conflicts over 16 keys
   // places that a wave's loads have in their groups of 16 keys
   constexpr int kPlaces = 16 / kLoadKeys > kW ? 16 / kLoadKeys / kW : 1;
   __shared__ __align__(1024) uint8_t tiles[2][2][kTileBytes];   // buffer, keys and values
@@ -306,7 +307,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
     for (int i = 0; i < kPlaces; ++i) {
       const int key = ((i * kW + wave) * kLoadKeys & 15) + lane / kPieces;
       const int swz = D == 64 ? (key >> 1) & 1 : key & (D / 32 - 1);   // values: 64-byte groups of pieces
-      k_at[i] = 2 * (key * D + 8 * (lane % kPieces ^ (key & 7)));
+      k_at[i] = 2 * (key * D + 8 * (lane % kPieces ^ (key & kKeySwap)));
       v_at[i] = 2 * (key * D + 8 * (lane % kPieces ^ swz << 2));
     }
     const int tok0 = u.j * tpb, n_tok = min(tpb, u.n - tok0), pos0 = u.base + tok0;
@@ -452,7 +453,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
           for (int i = 0; i < 16; ++i) s[r][i] = 0;
         // Operands are read kAhead products before they are used.
         const uint8_t* kp = &tiles[buf][0][(32 * sub + (ln & 31)) * D * 2];
-        auto key_part = [&](int i) { return *reinterpret_cast<const uint4*>(kp + (((2 * i + hl) ^ (ln & 7)) << 4)); };
+        auto key_part = [&](int i) { return *reinterpret_cast<const uint4*>(kp + (((2 * i + hl) ^ (ln & kKeySwap)) << 4)); };
         if constexpr (D > 64) __builtin_amdgcn_s_setprio(1);   // the wave in its products first
         uint4 kf[kAhead];
 #pragma unroll
