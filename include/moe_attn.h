@@ -93,9 +93,9 @@ typedef struct {
 /* Writes the n_tokens (up to 2^20) new tokens' keys and values into the cache;
  * seq_off NULL: one token for each sequence (n_tokens == batch).  With q, also
  * writes q_out [n_tokens][q_heads][head_dim] (16-byte aligned; q itself where q
- * lies like that).  Norms (device fp32 [head_dim]) and freq (device fp64
- * [rot_dim / 2], radians per position) may be NULL; rot_dim: a multiple of 16 up
- * to head_dim (0: none).  v is copied.  Arithmetic is fp32 (the angles fp64) and
+ * lies like that).  Norms (device fp32 [head_dim], 16-byte aligned) and freq
+ * (device fp64 [rot_dim / 2], radians per position) may be NULL; rot_dim: a
+ * multiple of 16 up to head_dim (0: none).  v is copied.  Arithmetic is fp32 (the angles fp64) and
  * each value is rounded once; a row whose sum of squares overflows fp32 counts
  * as zero.  Tokens without a position (more new tokens than the length) are
  * left out, their rows of q_out included. */
@@ -105,9 +105,9 @@ moe_status moe_kv_append(const moe_attn_desc* desc, const moe_kv_cache* cache, c
                          const float* k_norm_or_null, float eps, const double* freq_or_null, int32_t rot_dim,
                          moe_stream stream);
 
-/* Bytes of workspace (256-byte aligned) that moe_attn_decode (n_tokens = batch)
- * and moe_attn_prefill of up to n_tokens tokens need.  The workspace is only
- * used while a call runs. */
+/* Bytes of workspace (256-byte aligned) that moe_attn_decode (n_tokens 0) and
+ * moe_attn_prefill of up to n_tokens tokens need: up to 17 MB for the one, up to
+ * 136 MB for the other.  The workspace is only used while a call runs. */
 moe_status moe_attn_workspace_bytes(const moe_attn_desc* desc, int32_t n_tokens, size_t* bytes);
 
 /* Attention of the last token of every sequence: q, gate rows [batch], o

@@ -22,6 +22,14 @@
 // up the parts.  A unit counts kStart keys more than it has, for its begin and
 // end.  Every workgroup works out its run from the lengths and offsets on the
 // device, so a captured call follows them.
+//
+// One prompt of 8192 tokens, 16 query and 2 key heads of 256: 516 to 530 us by
+// box, 1040 to 1065 TFLOP/s (a library product of 8192^3 reaches 1236 here).  The
+// matrix cores are busy 54% and the vector units 48% of the cycles, and the
+// chip's power sets the clock: keys and values of 0 take 462 us.  12 prompts of
+// 6001 tokens: 105 us here (a unit's begin and end cost what 5 tiles do, of which
+// it has 8) and 25 in k_attn_join (134 MB of parts).  Five drafted tokens over
+// 4096: 18 and 6, latency.
 #include "attn.h"
 
 namespace moe {
@@ -30,7 +38,9 @@ namespace {
 constexpr int kRows = 256;                  // rows of a unit
 constexpr int kKeys = 64, kKeysLog = 6;     // keys of a tile
 constexpr int kMaxUnits = 1 << 22;
-constexpr int kStart = 384;                 // a unit's begin and end in keys
+// A unit's begin and end in keys (192, 320, 448, 640: 159, 139, 128, 137 us for 12 prompts of 6001 tokens, 105, 84, 88, 88
+// for 2048 tokens).
+constexpr int kStart = 384;
 constexpr int kRunLog = 7;                  // shortest run, in keys
 
 // Two 32-row tiles to a wave where a head is narrow enough: the registers of

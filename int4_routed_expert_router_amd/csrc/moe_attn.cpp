@@ -114,7 +114,8 @@ extern "C" moe_status moe_kv_append(const moe_attn_desc* d, const moe_kv_cache* 
   if (q && (!q_out || !at_aligned(q_out, 16)))
     return set_error(MOE_EINVAL, "q_out must be a 16-byte aligned device pointer");
   if (!q && (q_out || q_norm)) return set_error(MOE_EINVAL, "q_out and q_norm need q");
-  if (!at_aligned(q_norm, 4) || !at_aligned(k_norm, 4)) return set_error(MOE_EINVAL, "norms must be 4-byte aligned");
+  if (!at_aligned(q_norm, 16) || !at_aligned(k_norm, 16))
+    return set_error(MOE_EINVAL, "norms must be 16-byte aligned");
   if ((q_norm || k_norm) && !(eps >= 0 && std::isfinite(eps)))
     return set_error(MOE_EINVAL, "eps must be finite and not negative");
   if (rot_dim && (!freq || !at_aligned(freq, 8)))

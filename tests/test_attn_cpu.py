@@ -100,7 +100,7 @@ def test_bad_append_arguments():
     assert append(freq=None) == -1 and append(freq=4100) == -1
     assert append(q_out=None) == -1 and append(q_out=4104) == -1
     assert append(q=None) == -1 and append(q=None, q_out=None, q_norm=4096) == -1
-    assert append(q_norm=4098) == -1 and append(k_norm=4098) == -1
+    assert append(q_norm=4104) == -1 and append(k_norm=4104) == -1
     for eps in (-1.0, float("nan"), float("inf")):
         assert append(k_norm=4096, eps=eps) == -1
     for r in ((4104, 256, 256), (None, 256, 256)):
