@@ -47,8 +47,9 @@
  * whole batch, so a token's results may differ in their last bits between
  * batches.  Each output is rounded once to act_dtype.  A non-finite key or
  * value makes the results of the tokens that see it unusable (a score of
- * -infinity counts as a weight of 0; a row with no other gives 0), and so do values
-whose sum of magnitudes over the positions that a token sees leaves fp32's range.
+ * -infinity counts as a weight of 0; a row with no other gives 0), and so do
+ * values whose sum of magnitudes over the positions that a token sees leaves
+ * fp32's range.
  */
 #ifndef MOE_AMD_MOE_ATTN_H
 #define MOE_AMD_MOE_ATTN_H
@@ -106,8 +107,8 @@ moe_status moe_kv_append(const moe_attn_desc* desc, const moe_kv_cache* cache, c
                          moe_stream stream);
 
 /* Bytes of workspace (256-byte aligned) that moe_attn_decode (n_tokens 0) and
- * moe_attn_prefill of up to n_tokens tokens need: up to 17 MB for the one, up to
- * 136 MB for the other.  The workspace is only used while a call runs. */
+ * moe_attn_prefill of up to n_tokens tokens need: up to 9 MB for the one, up to
+ * 137 MB for the other.  The workspace is only used while a call runs. */
 moe_status moe_attn_workspace_bytes(const moe_attn_desc* desc, int32_t n_tokens, size_t* bytes);
 
 /* Attention of the last token of every sequence: q, gate rows [batch], o

@@ -7,7 +7,7 @@
 // lanes; all their loads leave before the token's sequence, position and page
 // are looked up.
 //
-// One token, 16 and 2 heads of 256: 3.4 us, latency of the look-up's loads and
+// One token, 16 and 2 heads of 256: 2.9 to 3.4 us, latency of the look-up's loads and
 // the launch.  8191 tokens of 5 sequences: 49 us, 168 MB at 3.4 TB/s, of which a
 // copy without norms and rotation takes 42 (rows of 512 bytes from every other
 // 512 bytes of a projection's output, to pages); with every head its own lanes

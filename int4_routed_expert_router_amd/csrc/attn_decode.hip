@@ -25,8 +25,8 @@
 // captured call follows them.
 //
 // Bound by the read of keys and values.  One sequence of 262143 positions, 2 key
-// heads of 256 (537 MB): 84 us here and 5 in k_join, 6.0 TB/s in all, what a
-// plain streaming read reaches; 64 sequences of up to 8192 (568 MB): 92 and 6.
+// heads of 256 (537 MB): 84 us here and 5 in k_join, 6.0 TB/s in all; a
+// plain streaming read of 1 GiB reaches 5.8 to 6.0; 64 sequences of up to 8192 (568 MB): 92 and 6.
 // What carried it from 121 us: no register spills (one wave to a SIMD at 256
 // dimensions, 102 to 90), one round of 256 workgroups (117 to 102), loads past
 // the caches (121 to 117).  A few positions: 8.6 us, four loads that wait for
@@ -66,7 +66,8 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 
 __device__ __forceinline__ int tiles_of(int len) { return (len + kTile - 1) >> kTileLog; }
 // A unit (a sequence's key head) costs two for each tile and one for its begin
-// and end (2 to 3 us, a tile takes 5); tiles that lie before position v of that.
+// and end (64 sequences of up to 8192: 98.6 us, without it 107); tiles that lie
+// before position v of that.
 __device__ __forceinline__ uint32_t cost_of(int len) { return len > 0 ? 2 * tiles_of(len) + 1 : 0; }
 __device__ __forceinline__ int tile_at(uint32_t v, int n_tiles) { return min(static_cast<int>(v >> 1), n_tiles); }
 

@@ -23,13 +23,13 @@
 // end.  Every workgroup works out its run from the lengths and offsets on the
 // device, so a captured call follows them.
 //
-// One prompt of 8192 tokens, 16 query and 2 key heads of 256: 516 to 530 us by
-// box, 1040 to 1065 TFLOP/s (a library product of 8192^3 reaches 1236 here).  The
-// matrix cores are busy 54% and the vector units 48% of the cycles, and the
-// chip's power sets the clock: keys and values of 0 take 462 us.  12 prompts of
-// 6001 tokens: 105 us here (a unit's begin and end cost what 5 tiles do, of which
-// it has 8) and 25 in k_attn_join (134 MB of parts).  Five drafted tokens over
-// 4096: 18 and 6, latency.
+// One prompt of 8192 tokens, 16 query and 2 key heads of 256: 523 us, 1050
+// TFLOP/s (a library product of 8192^3 reaches 1240 on the same card), once it has
+// run some 20 times; the first 20 runs take 600 each.  The matrix cores are busy
+// 54% and the vector units 48% of the cycles.  Keys and values of 0 take 442 us
+// with the same products, so that the data's part in it is 80 us, by power as it
+// seems.  12 prompts of 6001 tokens: 122 us with k_attn_join, which reads up to
+// 134 MB of parts in 25.  Five drafted tokens over 4096: 18 and 6, latency.
 #include "attn.h"
 
 namespace moe {
@@ -38,9 +38,10 @@ namespace {
 constexpr int kRows = 256;                  // rows of a unit
 constexpr int kKeys = 64, kKeysLog = 6;     // keys of a tile
 constexpr int kMaxUnits = 1 << 22;
-// A unit's begin and end in keys (192, 320, 448, 640: 159, 139, 128, 137 us for 12 prompts of 6001 tokens, 105, 84, 88, 88
-// for 2048 tokens).
-constexpr int kStart = 384;
+// A unit's begin and end in keys.  256, 320, 384, 448, 512: 135.7, 131.7, 126.4, 121.9, 122.4 us for 12 prompts of 6001
+// tokens; 84.5, 78.5, 80.2, 82.7, 79.9 for 2048 tokens; 39.9, 40.6, 41.4, 40.3, 40.2 for 512; 98.1, 100.3, 101.4, 100.5,
+// 103.2 for 2 x 4096 tokens of 8 key heads; 143 for 4 turns of 1023 over 12345 with each.
+constexpr int kStart = 512;
 constexpr int kRunLog = 7;                  // shortest run, in keys
 
 // Two 32-row tiles to a wave where a head is narrow enough: the registers of
