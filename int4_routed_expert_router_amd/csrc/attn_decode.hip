@@ -26,11 +26,12 @@
 //
 // Bound by the read of keys and values.  One sequence of 262143 positions, 2 key
 // heads of 256 (537 MB): 84 us here and 5 in k_join, 6.0 TB/s in all; a
-// plain streaming read of 1 GiB reaches 5.8 to 6.0; 64 sequences of up to 8192 (568 MB): 92 and 6.
+// plain streaming read of 1 GiB reaches 5.8 to 6.0, and the counters show 537 MB.
+// 64 sequences of up to 8192 (568 MB): 92 and 6.
 // What carried it from 121 us: no register spills (one wave to a SIMD at 256
 // dimensions, 102 to 90), one round of 256 workgroups (117 to 102), loads past
-// the caches (121 to 117).  A few positions: 8.6 us, four loads that wait for
-// each other (length, page, keys, merge) and the first fetch of the code.
+// the caches (121 to 117).  A few positions: 8.6 to 9.0 us, loads that wait for
+// each other (length, page, keys).
 #include "attn.h"
 
 namespace moe {
