@@ -24,11 +24,12 @@
 // device, so a captured call follows them.
 //
 // One prompt of 8192 tokens, 16 query and 2 key heads of 256: 523 us, 1050
-// TFLOP/s (a library product of 8192^3 reaches 1240 to 1250), once it has
-// run some 20 times; the first 20 runs take 600 each.  The matrix cores are busy
-// 54% and the vector units 48% of the cycles.  Keys and values of 0 take 442 us
-// with the same products: part of it follows the data, by power as it seems.  12 prompts of 6001 tokens: 122 us with k_attn_join, which reads up to
-// 134 MB of parts in 25.  Five drafted tokens over 4096: 18 and 6, latency.
+// TFLOP/s (a library product of 8192^3 reaches 1240 to 1250), once it has run some
+// 20 times; the first 20 runs take 600 each.  The matrix cores are busy 54% and
+// the vector units 48% of the cycles.  Keys and values of 0 take 442 us with the
+// same products: part of it follows the data, by power as it seems.  12 prompts
+// of 6001 tokens: 121 us with k_attn_join, which reads up to 134 MB of parts in
+// 24.  Five drafted tokens over 4096: 18 and 7, latency.
 #include "attn.h"
 
 namespace moe {
