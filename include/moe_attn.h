@@ -40,7 +40,8 @@
  * as its nearest end, and an end before its start as no tokens: no access
  * leaves the buffers, but where offsets decrease the results are not defined.
  * Rows outside every sequence are left as they are.  A row that sees no
- * position (length 0, or fewer positions than new tokens) gives 0.
+ * position (length 0, fewer positions than new tokens, no page that is one)
+ * gives 0, whatever its gate is.
  *
  * Sums, maxima and the softmax's sums are fp32 in a fixed order (bitwise
  * repeatable); the split of a long sequence over workgroups depends on the

@@ -99,15 +99,17 @@ __device__ __forceinline__ int64_t row_at(int t, int32_t ts, int h, int32_t hs) 
   return static_cast<int64_t>(t) * ts + static_cast<int64_t>(h) * hs;
 }
 
-// Four neighbouring normalised values of a row and head with their gates, if there are any.
+// Four neighbouring normalised values of a row and head with their gates, if
+// there are any; a row that sees no position is 0 whatever its gate is.
 __device__ __forceinline__ uint2 gates_of(const AttnArgs& a, int t, int h, int d) {
   return a.gate ? *reinterpret_cast<const uint2*>(a.gate + row_at(t, a.g_ts, h, a.g_hs) + d) : make_uint2(0, 0);
 }
 template <int ACT>
-__device__ __forceinline__ void store_row(const AttnArgs& a, int t, int h, int D, int d, f32x4_t v, uint2 g) {
+__device__ __forceinline__ void store_row(const AttnArgs& a, int t, int h, int D, int d, f32x4_t v, uint2 g, bool none) {
   if (a.gate) {
     v[0] *= sigmoid(act_to_f32<ACT>(g.x & 0xFFFFu)), v[1] *= sigmoid(act_to_f32<ACT>(g.x >> 16));
     v[2] *= sigmoid(act_to_f32<ACT>(g.y & 0xFFFFu)), v[3] *= sigmoid(act_to_f32<ACT>(g.y >> 16));
+    if (none) v = f32x4_t{0, 0, 0, 0};
   }
   *reinterpret_cast<uint2*>(a.o + (static_cast<int64_t>(t) * a.Hq + h) * D + d) =
       make_uint2(pack2<ACT>(v[0], v[1]), pack2<ACT>(v[2], v[3]));

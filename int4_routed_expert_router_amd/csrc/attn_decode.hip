@@ -374,7 +374,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void k_attn_decode(AttnArgs 
       }
       if (whole) {
         x *= lsum != 0 ? 1.0f / lsum : 0.0f;
-        store_row<ACT>(a, cur.b, cur.h * group + row, D, d, x, gates[i]);
+        store_row<ACT>(a, cur.b, cur.h * group + row, D, d, x, gates[i], lsum == 0);
       } else {
         *reinterpret_cast<f32x4_t*>(part_o + (slot * 16 + row) * D + d) = x;
         if (d == 0) part_ml[slot * 16 + row] = make_float2(mx, lsum);
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, const uint8_t* ws) {
       }
       if (tid % lanes == 0 && piece < to) {
         x *= l != 0 ? 1.0f / l : 0.0f;
-        store_row<ACT>(a, b, h * group + row, D, d, x, gates_of(a, b, h * group + row, d));
+        store_row<ACT>(a, b, h * group + row, D, d, x, gates_of(a, b, h * group + row, d), l == 0);
       }
       __syncthreads();
     }

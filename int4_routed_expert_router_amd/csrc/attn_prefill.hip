@@ -573,6 +573,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
 #pragma unroll
       for (int r = 0; r < kT; ++r) {
         const float sum = pair_sum(l[r]), inv = !whole ? 1.0f : sum != 0 ? 1.0f / sum : 0.0f;
+        const uint32_t none = static_cast<uint32_t>(__ballot(sum == 0));   // of the 32 rows
         if (!whole && ln < 32 && row_of(r, ln).real)
           reinterpret_cast<float2*>(ws + ml_at(S::kRuns))[static_cast<size_t>(slot) * held + row_of(r, ln).row] = make_float2(mx[r], sum);
 #pragma unroll
@@ -607,7 +608,8 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
               }
 #pragma unroll
               for (int e = 0; e < kBatch; ++e)
-                if (w[e].real) store_row<ACT>(a, u.begin + tok0 + w[e].tok, w[e].head, D, d, x[e], g[e]);
+                if (w[e].real) store_row<ACT>(a, u.begin + tok0 + w[e].tok, w[e].head, D, d, x[e], g[e],
+                                              none >> (i + e * kRowsAtOnce) & 1);
             } else {
 #pragma unroll
               for (int e = 0; e < kBatch; ++e)
@@ -637,7 +639,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
 
 // Adds up the parts of units that several runs hold: the workgroups of a unit's
 // runs share its outputs, four neighbouring ones to a piece, kSlices workgroups
-// to a part.  Also writes the zeros of rows that have no position.
+// to a part.  Also writes the zeros of the blocks that see no position: they are no units.
 constexpr int kSlices = 8;
 template <int ACT, class S>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, const uint8_t* ws) {
@@ -690,17 +692,16 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, const uint8_t* ws
           const int t = row / group;
           const int hq = u.h * group + row - t * group;
           store_row<ACT>(a, u.begin + tok0 + t, hq, D, d, x * (l != 0 ? 1.0f / l : 0.0f),
-                            gates_of(a, u.begin + tok0 + t, hq, d));
+                            gates_of(a, u.begin + tok0 + t, hq, d), l == 0);
         }
       }
     }
   }
   for (int b = w * kSlices + blockIdx.y; b < a.B; b += gridDim.x * kSlices) {
-    int begin, end;
-    seq_rows(a.off, b, a.N, begin, end);
-    const int none = min(end - begin - seq_length(a.length, b, a.max_pages, a.page_log), end - begin);
-    for (int64_t i = 8 * threadIdx.x; i < static_cast<int64_t>(max(none, 0)) * a.Hq * D; i += 2048)
-      *reinterpret_cast<uint4*>(a.o + static_cast<size_t>(begin) * a.Hq * D + i) = make_uint4(0, 0, 0, 0);
+    Seq s;
+    s.load(a, b, tpb);
+    for (int64_t i = 8 * threadIdx.x; i < static_cast<int64_t>(min(s.first * tpb, s.n)) * a.Hq * D; i += 2048)
+      *reinterpret_cast<uint4*>(a.o + static_cast<size_t>(s.begin) * a.Hq * D + i) = make_uint4(0, 0, 0, 0);
   }
 }
 
