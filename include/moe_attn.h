@@ -49,8 +49,9 @@
  * batches.  Each output is rounded once to act_dtype.  A non-finite key or
  * value makes the results of the tokens that see it unusable (a score of
  * -infinity counts as a weight of 0; a row with no other gives 0), and so do
- * values whose sum of magnitudes over the positions that a token sees leaves
- * fp32's range.
+ * products q . k or scores that leave fp32's range, and values whose sum of
+ * magnitudes over the positions that a token sees does.  Scores so large that
+ * fp32 holds no digits behind their point still give means of values.
  */
 #ifndef MOE_AMD_MOE_ATTN_H
 #define MOE_AMD_MOE_ATTN_H

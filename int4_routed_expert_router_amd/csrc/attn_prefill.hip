@@ -371,10 +371,10 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
     const int high = wave * kT * 32 / group < n_tok ? __builtin_amdgcn_readlane(pos[kT - 1], 31) : -1;
 
     f32x16_t o[kT][kBlocks];
-    float mx[kT], l[kT];
+    float ref[kT], l[kT];
 #pragma unroll
     for (int r = 0; r < kT; ++r) {
-      mx[r] = -INFINITY, l[r] = 0;
+      ref[r] = -INFINITY, l[r] = 0;
 #pragma unroll
       for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
@@ -499,22 +499,41 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
           float top = s[r][0];
 #pragma unroll
           for (int i = 1; i < 16; ++i) top = fmaxf(top, s[r][i]);
-          top = pair_max(top) * c;
-          // The reference for the exponents moves only when a weight would pass 2^8:
-          // the sums are fp32, and the row's result does not depend on it otherwise.
-          const bool grow = top > mx[r] + 8.0f;
-          if (__any(grow)) {
-            const float next = grow ? top : mx[r], base = next == -INFINITY ? 0.0f : next;
-            const float f = __builtin_amdgcn_exp2f(mx[r] - base);
-            mx[r] = next;
+          // Weights are 2^(z - ref).  The reference moves only when one would pass 2^8 of
+          // them: the sums are fp32, and the row's result does not depend on it otherwise.
+          bool grow;
+          {
+#pragma clang fp contract(off)
+            top = pair_max(top) * c;
+            grow = top - ref[r] > 8.0f + kShift<ACT>;
+          }
+          float base = ref[r] == -INFINITY ? 0.0f : ref[r];
+          // (and what follows them, where a row's reference is far from 0 or not set)
+          if (__any(grow | (fabsf(ref[r]) > 0x1p21f))) {
+            const float next = grow ? top - kShift<ACT> : ref[r];
+            base = next == -INFINITY ? 0.0f : next;
+            const float f = __builtin_amdgcn_exp2f(ref[r] - base);
+            ref[r] = next;
             const float g = grow ? f : 1.0f;
             l[r] *= g;
 #pragma unroll
             for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
               for (int j = 0; j < 16; ++j) o[r][i][j] *= g;
+            if (fabsf(base) > 0x1p21f) {
+              // Scores without digits behind the point: a fused s c - base differs from the
+              // rounded s c that the reference is one of by up to half a step, which is no
+              // part of an exponent any more.  So the rounded ones, as products of c again.
+#pragma clang fp contract(off)
+              const float per_c = 1.0f / c;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float z = s[r][i] * c, e = z - base;
+                s[r][i] = e * per_c;
+              }
+              base = 0.0f;
+            }
           }
-          const float base = (mx[r] == -INFINITY ? 0.0f : mx[r]) - kShift<ACT>;
           float sum = 0;
           uint32_t w[8];
 #pragma unroll
@@ -575,7 +594,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
         const float sum = pair_sum(l[r]), inv = !whole ? 1.0f : sum != 0 ? 1.0f / sum : 0.0f;
         const uint32_t none = static_cast<uint32_t>(__ballot(sum == 0));   // of the 32 rows
         if (!whole && ln < 32 && row_of(r, ln).real)
-          reinterpret_cast<float2*>(ws + ml_at(S::kRuns))[static_cast<size_t>(slot) * held + row_of(r, ln).row] = make_float2(mx[r], sum);
+          reinterpret_cast<float2*>(ws + ml_at(S::kRuns))[static_cast<size_t>(slot) * held + row_of(r, ln).row] = make_float2(ref[r], sum);
 #pragma unroll
         for (int d0 = 0; d0 < D; d0 += kWide) {
 #pragma unroll

@@ -40,3 +40,61 @@ def test_gates_of_rows_before_a_cut_unit(act, d):
     c.gate[:10] = float("nan")
     for _ in range(5):
         assert same_bits(c.run(), want)
+
+
+def between_the_values(c, o, decode, slack):
+    """Each output lies between the values that its row sees, up to slack of the largest."""
+    import torch
+    v, table, off = c.v.double(), c.table.cpu(), c.off.tolist()
+    for b, n in enumerate(c.total):
+        m = 1 if decode else c.new[b]
+        row0 = b if decode else off[b]
+        for i in range(m):
+            p = n - m + i
+            if p < 0:
+                continue
+            pos = torch.arange(p + 1)
+            seen = v[table[b, pos // c.page].long(), :, pos % c.page].repeat_interleave(c.q.shape[1] // v.shape[1], 1)
+            big = seen.abs().amax(0)
+            x = o[row0 + i].double()
+            assert ((x >= seen.amin(0) - slack * big) & (x <= seen.amax(0) + slack * big)).all(), (b, i)
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("exponent", range(20, 47, 2))
+def test_scores_of_many_digits(act, decode, exponent):
+    """Scores of some 2^exponent have no digits left that tell weights apart, but outputs are still means of values: a
+    weight's rounding (half a step of the type, and of the output) and below 2^-12 of fp32 sums of 200 terms."""
+    from attn_testlib import STEP
+    new, total = ([1] * 3, [150, 1, 70]) if decode else ([150, 1, 40], [150, 1, 70])
+    c = case(new, total, 4, 2, 64, 16, act, seed=exponent)
+    # |q k| is some 2^10 with 64 products of 1.5 each; then the scale
+    for form in range(2):
+        if form:   # every key of a head the same
+            c.k = c.k.clone()
+            for b, n in enumerate(total):
+                for p in range(n):
+                    c.k[c.table[b, p // 16].long(), :, p % 16] = c.k[c.table[b, 0].long(), :, 0]
+        c.scale = 2.0 ** (exponent - 4) * (1 + exponent / 64)
+        between_the_values(c, c.run(decode), decode, 2 * STEP[act] + 2.0 ** -12)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [128, 256])
+@pytest.mark.parametrize("step", [1, 2, 3, 8, 16])
+def test_large_scores_that_grow_by_single_steps(act, d, step):
+    # scores of 127 x 2^20 + 8 j, exact in fp32 (steps of 8); scaled by log2(e) they keep steps of 8
+    import torch
+    from attn_testlib import STEP
+    n = 160
+    c = case([n], [n], 2, 1, d, 32, act, seed=step)
+    c.scale = 1.0 / 1.44269504
+    c.q[:] = 0
+    c.q[:, :, :127] = 1024.0
+    c.q[:, :, 127] = 8.0
+    c.k[:] = 0
+    c.k[..., :127] = 1024.0
+    pos = torch.arange(n, device="cuda")
+    c.k[c.table[0, (pos // 32)].long(), 0, pos % 32, 127] = (pos // 32 * step).to(c.k.dtype)
+    between_the_values(c, c.run(), False, 2 * STEP[act] + 2.0 ** -12)
