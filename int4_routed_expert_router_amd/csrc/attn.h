@@ -81,8 +81,8 @@ __device__ __forceinline__ float quad_sum(float v) {
 }
 
 constexpr float kLog2e = 1.44269504f;
-// Softmax weights are held as 2^kShift exp(z - max): fp16 keeps its full
-// precision down to 2^-14, so a shift of 7 leaves 2^-21 of the largest weight.
+// Softmax weights in the decode kernel are 2^kShift exp(z - max): fp16 keeps its
+// full precision down to 2^-14, so a shift of 7 leaves 2^-21 of the largest weight.
 template <int ACT>
 constexpr float kShift = ACT == 2 ? 0.0f : 7.0f;
 __device__ __forceinline__ float sigmoid(float x) {

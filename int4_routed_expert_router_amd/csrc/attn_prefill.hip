@@ -254,6 +254,14 @@ __device__ bool next_unit(const AttnArgs& a, int tpb, Unit& u) {
   return false;
 }
 
+// A row's weights are 2^(z - ref), where ref is set to its largest z - kLift and
+// moves when a weight would pass 2^(kLift + 8).  fp16: 2^15 at most, and full
+// precision down to 2^-21 of the largest weight.  bf16: below 1 (2^-1 and the
+// rounding of large scores), so that no sum of weighted values passes that of the
+// values' magnitudes; its exponents reach as far as fp32's.
+template <int ACT>
+constexpr float kLift = ACT == 2 ? -9.0f : 7.0f;
+
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 // 16 bytes a lane from base + at to LDS address lds + 16 lane, behind the
@@ -499,18 +507,17 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
           float top = s[r][0];
 #pragma unroll
           for (int i = 1; i < 16; ++i) top = fmaxf(top, s[r][i]);
-          // Weights are 2^(z - ref).  The reference moves only when one would pass 2^8 of
-          // them: the sums are fp32, and the row's result does not depend on it otherwise.
+          // the sums are fp32, and the row's result does not depend on when ref moves
           bool grow;
           {
 #pragma clang fp contract(off)
             top = pair_max(top) * c;
-            grow = top - ref[r] > 8.0f + kShift<ACT>;
+            grow = top - ref[r] > kLift<ACT> + 8.0f;
           }
           float base = ref[r] == -INFINITY ? 0.0f : ref[r];
           // (and what follows them, where a row's reference is far from 0 or not set)
           if (__any(grow | (fabsf(ref[r]) > 0x1p21f))) {
-            const float next = grow ? top - kShift<ACT> : ref[r];
+            const float next = grow ? top - kLift<ACT> : ref[r];
             base = next == -INFINITY ? 0.0f : next;
             const float f = __builtin_amdgcn_exp2f(ref[r] - base);
             ref[r] = next;

@@ -98,3 +98,20 @@ def test_large_scores_that_grow_by_single_steps(act, d, step):
     pos = torch.arange(n, device="cuda")
     c.k[c.table[0, (pos // 32)].long(), 0, pos % 32, 127] = (pos // 32 * step).to(c.k.dtype)
     between_the_values(c, c.run(), False, 2 * STEP[act] + 2.0 ** -12)
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_values_whose_sum_just_fits(decode, d):
+    # 64 values of up to 2^121: their magnitudes add up to less than 2^127.  Scores rise by 5.5 (8 in powers of two).
+    n = 64
+    c = case([1] if decode else [n], [n], 2, 1, d, 16, "bf16", seed=33)
+    sign = 1 - 2 * (c.v.float() < 0).float()
+    c.v = (sign * 2.0 ** 121).to(c.v.dtype)
+    c.q[:] = 0
+    c.q[:, :, 0] = 1.0
+    for p in range(n):
+        c.k[c.table[0, p // 16].long(), 0, p % 16] = 0
+        c.k[c.table[0, p // 16].long(), 0, p % 16, 0] = 0.0 if p < 32 else 5.5
+    c.scale = 1.0
+    c.check(c.run(decode), decode)
