@@ -309,9 +309,9 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
   Part* parts = reinterpret_cast<Part*>(ws + sizeof(Header)) + 2 * run;
   if (cut && threadIdx.x < 2) parts[threadIdx.x].u.b = -1;
 
-  const uint32_t flip = a.scale < 0 ? 0x80008000u : 0u;
-  // scores are non-negative multiples of the products; a scale of 0 counts as 2^-126
-  const float c = fmaxf(fabsf(a.scale) * kLog2e, 1.17549435e-38f);
+  // scores are positive multiples of the products; for a scale of 0 the queries are 0
+  const uint32_t flip = a.scale < 0 ? 0x80008000u : 0u, keep = a.scale == 0 ? 0u : ~0u;
+  const float c = a.scale == 0 ? 1.0f : fabsf(a.scale) * kLog2e;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_address(&tiles[0][0][wave * 1024]));
   int turn = 0;   // place of the next tile in bad_key
   if (threadIdx.x == 0) bad_key[0] = bad_key[1] = INT_MAX;
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
         const uint4 v = *reinterpret_cast<const uint4*>(qp + 16 * i);
-        q[r][i] = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+        q[r][i] = make_uint4((v.x & keep) ^ flip, (v.y & keep) ^ flip, (v.z & keep) ^ flip, (v.w & keep) ^ flip);
       }
     }
     // of the wave's rows; no key at all where none of them is real

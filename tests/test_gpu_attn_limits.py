@@ -115,3 +115,21 @@ def test_values_whose_sum_just_fits(decode, d):
         c.k[c.table[0, p // 16].long(), 0, p % 16, 0] = 0.0 if p < 32 else 5.5
     c.scale = 1.0
     c.check(c.run(decode), decode)
+
+
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-39, -1e-39, 1e-44, 2.0 ** -127])
+def test_scales_of_none_and_subnormal_ones(decode, scale):
+    # products of 2^126 times the scale: 0.06 to 0.85
+    c = case([1] if decode else [40], [40], 2, 1, 64, 16, "bf16", seed=34)
+    c.q[:] = 0
+    c.q[:, 0, 3], c.q[:, 1, 5] = 2.0 ** 63, -2.0 ** 62
+    for p in range(40):
+        k = c.k[c.table[0, p // 16].long(), 0, p % 16]
+        k[:] = 0
+        k[3] = 2.0 ** 63 * (p % 3 - 1)
+        k[5] = 2.0 ** 63 * (p % 5 - 2)
+    c.scale = scale
+    # a subnormal scale has fewer digits: the float's own value is meant
+    c.scale = float(np.float32(scale))
+    c.check(c.run(decode), decode)
