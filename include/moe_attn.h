@@ -114,7 +114,7 @@ moe_status moe_kv_append(const moe_attn_desc* desc, const moe_kv_cache* cache, c
 moe_status moe_attn_workspace_bytes(const moe_attn_desc* desc, int32_t n_tokens, size_t* bytes);
 
 /* Attention of the last token of every sequence: q, gate rows [batch], o
- * [batch][q_heads][head_dim] (16-byte aligned).  scale: finite. */
+ * [batch][q_heads][head_dim] (16-byte aligned).  scale: finite, up to 2^127 either way. */
 moe_status moe_attn_decode(const moe_attn_desc* desc, const moe_kv_cache* cache, const moe_attn_rows* q,
                            const moe_attn_rows* gate_or_null, float scale, void* o, void* ws, size_t ws_bytes,
                            moe_stream stream);

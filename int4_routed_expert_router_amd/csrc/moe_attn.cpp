@@ -69,7 +69,7 @@ moe_status attend(const moe_attn_desc* d, const moe_kv_cache* c, const int32_t* 
   if (!st) st = check_rows("q", q);
   if (!st && gate) st = check_rows("gate", gate);
   if (st) return st;
-  if (!std::isfinite(scale)) return set_error(MOE_EINVAL, "scale must be finite");
+  if (!std::isfinite(scale * kLog2e)) return set_error(MOE_EINVAL, "scale must be finite and below 2^127");
   if (!decode && (!off || !at_aligned(off, 4)))
     return set_error(MOE_EINVAL, "seq_off must be a 4-byte aligned device pointer");
   if (!o || !at_aligned(o, 16)) return set_error(MOE_EINVAL, "o must be a 16-byte aligned device pointer");
