@@ -139,11 +139,20 @@ __global__ __launch_bounds__(256) void k_kv_append(AppendArgs a) {
       unpack8<ACT>(xv[i], x);
       unpack8<ACT>(yv[i], y);
       if (norm) {
-        float ss = 0;
+        auto mean_square = [&](float eps) {
+          float ss = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-        ss = head_sum<kLanes>(ss);
-        const float r = __builtin_amdgcn_rsqf(fmaf(ss, 1.0f / D, a.eps));   // the hardware's, within an ulp
+          for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+          return fmaf(head_sum<kLanes>(ss), 1.0f / D, eps);
+        };
+        float ms = mean_square(a.eps);
+        if (__any(ms < 0x1p-80f)) {   // rows whose squares leave fp32's range below, times 2^80
+          const float up = ms < 0x1p-80f ? 0x1p80f : 1.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] *= up, y[j] *= up;
+          ms = mean_square(a.eps * up * up);
+        }
+        const float r = __builtin_amdgcn_rsqf(ms);   // the hardware's, within an ulp
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           x[j] *= r * nx[j];

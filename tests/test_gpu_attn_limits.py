@@ -133,3 +133,33 @@ def test_scales_of_none_and_subnormal_ones(decode, scale):
     # a subnormal scale has fewer digits: the float's own value is meant
     c.scale = float(np.float32(scale))
     c.check(c.run(decode), decode)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-38, 1e-30, 1e-20])
+@pytest.mark.parametrize("n", [3, 1100])
+def test_norms_of_tiny_rows(act, eps, n):
+    import torch
+    from int4_routed_expert_router_amd import api
+    from oracle import attention_oracle as ao
+    from test_gpu_attn import append_inputs, close
+    hq, hk, d, page = 4, 2, 128, 64
+    q, k, v, qn, kn, freq = append_inputs(hq, hk, d, n, d, True, act, 35)
+    # from ordinary rows down to the type's smallest numbers (bf16 2^-133, fp16 2^-24)
+    low = 120 if act == "bf16" else 14
+    size = 2.0 ** -(torch.arange(n * hq, device="cuda").view(n, hq, 1) % 9 * low / 8)
+    q = (q.float() * size).to(q.dtype)
+    k = (k.float() * size[:, :hk]).to(k.dtype)
+    pages = -(-n // page)
+    kc = torch.zeros(pages, hk, page, d, dtype=q.dtype, device="cuda")
+    vc = torch.zeros_like(kc)
+    cache = api.KVCache(kc, vc, torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1),
+                        torch.tensor([n], dtype=torch.int32, device="cuda"))
+    off = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    qo = torch.empty(n, hq, d, dtype=q.dtype, device="cuda")
+    api.kv_append(cache, k, v, seq_off=off, q=q, q_out=qo, q_norm=qn, k_norm=kn, eps=eps, freq=freq)
+    f = lambda t: t.double().cpu().numpy()  # noqa: E731
+    e = float(np.float32(eps))
+    for i in range(n):
+        close(f(qo[i]), ao._head(f(q[i]), f(qn), e, f(freq), i), act)
+        close(f(kc[i // page, :, i % page]), ao._head(f(k[i]), f(kn), e, f(freq), i), act)
