@@ -157,7 +157,7 @@ __device__ bool begin_work(const AttnArgs& a, int tpb, Unit& u, bool& cut, Runs&
     s.load(a, 64 * c + lane, tpb);
     upto = wave_scan64(s.all(tpb));
     total += lane64(upto, 63);
-    int top = s.base + s.n, sum = s.blocks - s.first;
+    int sum = s.blocks - s.first, top = sum > 0 ? s.base + s.n : 0;   // positions of sequences with units
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) {
       top = max(top, __shfl_xor(top, m));

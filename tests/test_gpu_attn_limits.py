@@ -163,3 +163,16 @@ def test_norms_of_tiny_rows(act, eps, n):
     for i in range(n):
         close(f(qo[i]), ao._head(f(q[i]), f(qn), e, f(freq), i), act)
         close(f(kc[i // page, :, i % page]), ao._head(f(k[i]), f(kn), e, f(freq), i), act)
+
+
+@pytest.mark.parametrize("heads,d,n", [((16, 2), 256, 40), ((8, 8), 64, 40), ((4, 4), 128, 80)])
+def test_a_sequence_without_tokens_changes_nothing(heads, d, n):
+    # an even batch with and without a sequence of a long cache that has no new tokens
+    import torch
+    from int4_routed_expert_router_amd import api
+    c = case([300] * n + [0], [300] * n + [20000], *heads, d, 64, "bf16", seed=36)
+    with_it = c.run()
+    o = torch.full(c.q.shape, 7.0, dtype=c.q.dtype, device="cuda")
+    api.attn_prefill(api.KVCache(c.k, c.v, c.table[:n].contiguous(), c.length[:n].contiguous()), c.q, o,
+                     c.off[: n + 1].contiguous(), c.scale)
+    assert torch.equal(with_it, o)
