@@ -266,12 +266,15 @@ typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
 // 16 bytes a lane from base + at to LDS address lds + 16 lane, behind the
 // compiler's back: it would wait for every such copy before the next LDS read,
-// whichever buffer that reads.  landed() waits for the wave's own.
+// whichever buffer that reads.  landed() waits for the wave's own.  A memory
+// instruction reads a scalar register five wait states after a vector
+// instruction wrote it at the earliest, which the compiler does not look after
+// in here: the move and the s_nop before are that many.
 __device__ __forceinline__ void to_lds16(const void* base, uint32_t at, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(at), "s"(base), "s"(lds) : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(at), "s"(base), "s"(lds) : "memory", "m0");
 }
 __device__ __forceinline__ void to_lds16(const void* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory");
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory", "m0");
 }
 __device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
