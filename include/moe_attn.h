@@ -46,12 +46,15 @@
  * Sums, maxima and the softmax's sums are fp32 in a fixed order (bitwise
  * repeatable); the split of a long sequence over workgroups depends on the
  * whole batch, so a token's results may differ in their last bits between
- * batches.  Each output is rounded once to act_dtype.  A non-finite key or
- * value makes the results of the tokens that see it unusable (a score of
- * -infinity counts as a weight of 0; a row with no other gives 0), and so do
- * products q . k or scores that leave fp32's range, and values whose sum of
- * magnitudes over the positions that a token sees does.  Scores so large that
- * fp32 holds no digits behind their point still give means of values.
+ * batches.  Softmax weights meet the values as act_dtype in moe_attn_prefill
+ * (each off by up to half a step; their sum is that of the unrounded ones) and
+ * as the sum of two such numbers in moe_attn_decode.  Each output is rounded
+ * once to act_dtype.  A non-finite key or value makes the results of the tokens
+ * that see it unusable (a score of -infinity counts as a weight of 0; a row with
+ * no other gives 0), and so do products q . k or scores that leave fp32's range,
+ * and values whose sum of magnitudes over the positions that a token sees does.
+ * Scores so large that fp32 holds no digits behind their point still give means
+ * of values.
  */
 #ifndef MOE_AMD_MOE_ATTN_H
 #define MOE_AMD_MOE_ATTN_H

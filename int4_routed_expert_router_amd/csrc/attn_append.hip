@@ -8,17 +8,19 @@
 // are looked up.
 //
 // One token, 16 and 2 heads of 256: 2.9 to 3.4 us, latency of the look-up's loads and
-// the launch.  8191 tokens of 5 sequences: 49 us, 168 MB at 3.4 TB/s, of which a
+// the launch.  8191 tokens of 5 sequences: 50 us, 168 MB at 3.4 TB/s, of which a
 // copy without norms and rotation takes 42 (rows of 512 bytes from every other
 // 512 bytes of a projection's output, to pages); with every head its own lanes
-// (R = 1) 52.  Stores past the caches are 3 us faster here, but the attention
-// that follows reads what they wrote.
+// (R = 1) 52.  20 rows (16 + 2 + 2) take 20 of a workgroup's 32 places with R = 4:
+// the others load the last row and write nothing.  Stores past the caches are 3 us
+// faster here, but the attention that follows reads what they wrote.
 #include "attn.h"
 
 namespace moe {
 namespace {
 
-// From so many tokens on R = 4: 300 tokens take 7.0 us with R = 1 against 8.2, 1000 take 10.0 against 9.9, 8191 52 against 49.5.
+// From so many tokens on R = 4 (timed for 16 and 2 heads of 256): 300 tokens take 7.0 us with R = 1 against 8.2, 1000 take 10.0
+// against 9.9, 8191 52 against 49.5.
 constexpr int kManyTokens = 1024;
 
 template <int ACT>

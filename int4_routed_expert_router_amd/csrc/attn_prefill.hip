@@ -23,13 +23,18 @@
 // end.  Every workgroup works out its run from the lengths and offsets on the
 // device, so a captured call follows them.
 //
-// One prompt of 8192 tokens, 16 query and 2 key heads of 256: 523 us, 1050
-// TFLOP/s (a library product of 8192^3 reaches 1240 to 1250), once it has run some
-// 20 times; the first 20 runs take 600 each.  The matrix cores are busy 54% and
-// the vector units 48% of the cycles.  Keys and values of 0 take 442 us with the
-// same products: part of it follows the data, by power as it seems.  12 prompts
-// of 6001 tokens: 121 us with k_attn_join, which reads up to 134 MB of parts in
-// 24.  Five drafted tokens over 4096: 18 and 7, latency.
+// One prompt of 8192 tokens, 16 query and 2 key heads of 256: 520 to 540 us from
+// card to card, 1020 to 1060 TFLOP/s (a library product of 8192^3 reaches 1240 to
+// 1250), on a card at work.  After a pause its first 30 runs take 560 to 720, as
+// library products then take 840 to 1030 where they settle at 783; after 100 such
+// products the kernel is at its steady time from the first run on.  The matrix
+// cores are busy 53% and the vector units 48% of the cycles.  Keys and values of 0
+// take 442 us with the same products: part of it follows the data, by power as it
+// seems.  16 and 4 heads of 128: 329 us, matrix cores 46%, vector units 52%; of
+// 64: 210, 32% and 65% (a tile of scores has 16 exponentials to 8 products).
+// 12 prompts of 6001 tokens: 121 to 125 us with k_attn_join, which reads up to 134
+// MB of parts in 24.  Five drafted tokens over 4096: 19 and 6, latency (40 rows of
+// a unit's 256 are theirs).
 #include "attn.h"
 
 namespace moe {
@@ -40,7 +45,8 @@ constexpr int kKeys = 64, kKeysLog = 6;     // keys of a tile
 constexpr int kMaxUnits = 1 << 22;
 // A unit's begin and end in keys.  256, 320, 384, 448, 512: 135.7, 131.7, 126.4, 121.9, 122.4 us for 12 prompts of 6001
 // tokens; 84.5, 78.5, 80.2, 82.7, 79.9 for 2048 tokens; 39.9, 40.6, 41.4, 40.3, 40.2 for 512; 98.1, 100.3, 101.4, 100.5,
-// 103.2 for 2 x 4096 tokens of 8 key heads; 143 for 4 turns of 1023 over 12345 with each.
+// 103.2 for 2 prompts of 4096 tokens in all, 8 key heads; 143 for 4 turns of 1023 over 12345 with each.  All with heads of
+// 256: narrower ones were not swept.
 constexpr int kStart = 512;
 constexpr int kRunLog = 7;                  // shortest run, in keys
 
@@ -518,7 +524,8 @@ __global__ __launch_bounds__(64 * S::kW, 2) void k_attn_prefill(AttnArgs a, uint
             grow = top - ref[r] > kLift<ACT> + 8.0f;
           }
           float base = ref[r] == -INFINITY ? 0.0f : ref[r];
-          // (and what follows them, where a row's reference is far from 0 or not set)
+          // (and what follows them, where a row's reference is far from 0 or not set: looking
+          // costs 1%, 528 us to 533 for 8192 tokens)
           if (__any(grow | (fabsf(ref[r]) > 0x1p21f))) {
             const float next = grow ? top - kLift<ACT> : ref[r];
             base = next == -INFINITY ? 0.0f : next;

@@ -199,7 +199,7 @@ def test_decode_of_ragged_batches_at_its_own_precision(shape, act):
 def test_decode_weights_are_held_to_more_than_the_type(act, d, page, n):
     """Two weights, 1 and 0.75 + w, on values -0.75 and 1 in turn.  w is three eighths of the type's steps there, so that it
     is what rounding the weight to the type loses: the result, w / 1.75, would be 0 (bf16 8.4e-4, fp16 1.0e-4, against an
-    allowed error of 4.5e-5 and 3.4e-5 at 64 positions of 256)."""
+    allowed error of 4.9e-5 and 3.3e-5 at 64 positions of 256)."""
     import torch
     from attn_testlib import STEP
     c = case([1] * 2, [n, n], 4, 2, d, page, act, seed=51)
