@@ -215,3 +215,131 @@ def test_decode_weights_are_held_to_more_than_the_type(act, d, page, n):
         c.k[pages, :, pos % page, 3] = odd[:, None]
         c.v[pages, :, pos % page] = torch.where(odd > 0, 1.0, -0.75).to(c.v.dtype)[:, None, None]
     c.check(c.run(decode=True), decode=True)
+
+
+# ------------------------------------------------------------------ the largest calls
+@pytest.mark.parametrize("decode", [True, False])
+@pytest.mark.parametrize("B", [5000, 65535])
+def test_attention_of_the_largest_batches(decode, B):
+    # most places of the batch hold nothing
+    rng = np.random.default_rng(B)
+    live = np.sort(rng.choice(B, 200, replace=False))
+    live[0], live[-1] = 0, B - 1
+    total = np.zeros(B, np.int64)
+    total[live] = rng.integers(1, 40, 200)
+    new = np.ones(B, np.int64) if decode else np.zeros(B, np.int64)
+    if not decode:
+        new[live] = rng.integers(1, 5, 200)              # some with more than they have positions
+    c = case(new.tolist(), total.tolist(), 2, 1, 64, 16, "f16", gate=True, seed=60)
+    c.check(c.run(decode), decode)
+
+
+def test_causal_attention_of_the_most_tokens():
+    # 2^20 rows, 65535 sequences of 16 that share a page: each sequence's rows are the first one's, up to the last bits
+    import torch
+    from attn_testlib import STEP
+    from int4_routed_expert_router_amd import api
+    c = case([16], [16], 2, 1, 64, 16, "bf16", seed=61)
+    one = c.run()
+    c.check(one)
+    B, N = 65535, 1 << 20
+    q = c.q[:16].repeat(N // 16, 1, 1)
+    o = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    table = c.table[:, :1].repeat(B, 1).contiguous()
+    off = torch.arange(B + 1, dtype=torch.int32, device="cuda") * 16
+    api.attn_prefill(api.KVCache(c.k, c.v, table, torch.full((B,), 16, dtype=torch.int32, device="cuda")), q, o, off, c.scale)
+    want = one[:16].double()
+    got = o[: 16 * B].view(B, 16, 2, 64)
+    big = c.v[c.table[0, 0].long()].double().abs().max()
+    # two results within a rounding of the output and of the weights of the same value each
+    assert (got - want).abs().amax(0).le(2 * STEP["bf16"] * (want.abs() + big) + 2.0 ** -14).all()
+    assert (o[16 * B :] == 7).all()
+
+
+@pytest.mark.parametrize("B", [1100, 65535])
+def test_append_of_one_token_each(B):
+    # no offsets: the form for many tokens, and its twin with offsets
+    import torch
+    from int4_routed_expert_router_amd import api
+    from test_gpu_attn import append_inputs
+    hq, hk, d, page = (16, 2, 256, 16) if B < 2000 else (40, 8, 64, 16)
+    q, k, v, qn, kn, freq = append_inputs(hq, hk, d, B, d // 2, True, "bf16", 62)
+    table = torch.randperm(B, device="cuda").int().view(B, 1)
+    length = torch.randint(0, 17, (B,), device="cuda").int()         # 0: no place
+    outs = []
+    for off in (None, torch.arange(B + 1, dtype=torch.int32, device="cuda")):
+        kc = torch.zeros(B, hk, page, d, dtype=q.dtype, device="cuda")
+        vc, qo = torch.zeros_like(kc), torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+        api.kv_append(api.KVCache(kc, vc, table, length), k, v, seq_off=off, q=q, q_out=qo, q_norm=qn, k_norm=kn, freq=freq)
+        outs.append((qo, kc, vc))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    qo, kc, vc = outs[0]
+    here = length > 0
+    assert (qo[~here] == 7).all() and (qo[here] != 7).any()
+    assert torch.equal(vc[table[here, 0].long(), :, (length[here] - 1).long()], v[here])
+    assert int((vc != 0).any(-1).any(1).sum()) == int(here.sum())
+    # against a sequence at a time, where the other form is taken
+    for b in torch.nonzero(here)[:: max(B // 20, 1), 0].tolist():
+        k1, v1 = torch.zeros_like(kc[:1]), torch.zeros_like(kc[:1])
+        q1 = torch.empty(1, hq, d, dtype=q.dtype, device="cuda")
+        api.kv_append(api.KVCache(k1, v1, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), length[b : b + 1]), k[b : b + 1],
+                      v[b : b + 1], q=q[b : b + 1], q_out=q1, q_norm=qn, k_norm=kn, freq=freq)
+        page_of = int(table[b, 0])
+        assert torch.equal(q1[0], qo[b]) and torch.equal(k1[0], kc[page_of]) and torch.equal(v1[0], vc[page_of])
+
+
+@pytest.mark.parametrize("n", [40, 1100])
+def test_append_beyond_32_bits(n):
+    # pages whose elements lie beyond 2^32, the same bits as in a small cache
+    import torch
+    from int4_routed_expert_router_amd import api
+    from test_gpu_attn import append_inputs
+    hq, hk, d, page = 16, 2, 256, 64
+    q, k, v, qn, kn, freq = append_inputs(hq, hk, d, n, 64, True, "bf16", 63)
+    m = -(-n // page)
+    off, length = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n], [n]))
+    got = []
+    for pages in (m, (1 << 32) // (hk * page * d) + m):
+        kc = torch.zeros(pages, hk, page, d, dtype=q.dtype, device="cuda")
+        vc = torch.zeros_like(kc)
+        table = torch.arange(pages - m, pages, dtype=torch.int32, device="cuda").view(1, m)
+        qo = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+        api.kv_append(api.KVCache(kc, vc, table, length), k, v, seq_off=off, q=q, q_out=qo, q_norm=qn, k_norm=kn, freq=freq)
+        got.append((qo, kc[pages - m :].clone(), vc[pages - m :].clone()))
+        assert not kc[: pages - m].any()
+        del kc, vc
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.parametrize("decode", [True, False])
+def test_rows_beyond_32_bits(decode):
+    # tokens 2^30 elements apart
+    import torch
+    from int4_routed_expert_router_amd import api
+    n, hq, hk, d = 4, 4, 2, 64
+    c = case([1] * n if decode else [n], [30, 7, 64, 21] if decode else [90], hq, hk, d, 16, "f16", gate=True, seed=64)
+    want = c.run(decode)
+    c.check(want, decode)
+    step = (1 << 30) + 8
+    wide = torch.zeros(3 * step + (2 * hq + 2 * hk) * d, dtype=torch.float16, device="cuda")
+
+    def far(t, at):
+        view = wide.as_strided((n, t.shape[1], d), (step, d, 1), at)
+        view.copy_(t[:n])
+        return view
+
+    q, gate = far(c.q, 0), far(c.gate, hq * d)
+    o = torch.full((n, hq, d), 7.0, dtype=torch.float16, device="cuda")
+    if decode:
+        api.attn_decode(c.cache(), q, o, c.scale, gate=gate)
+    else:
+        api.attn_prefill(c.cache(), q, o, c.off, c.scale, gate=gate)
+    assert torch.equal(o, want[:n])
+    kv = torch.randn(n, 2 * hk, d, device="cuda").half()
+    k, v = far(kv[:, :hk], 2 * hq * d), far(kv[:, hk:], (2 * hq + hk) * d)
+    outs = []
+    for a, b in ((k, v), (kv[:, :hk], kv[:, hk:])):
+        kc, vc = c.k.clone(), c.v.clone()
+        api.kv_append(api.KVCache(kc, vc, c.table, c.length), a, b, seq_off=None if decode else c.off)
+        outs.append((kc.view(torch.int16), vc.view(torch.int16)))
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and not torch.equal(outs[0][1], c.v.view(torch.int16))
